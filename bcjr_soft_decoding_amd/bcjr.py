@@ -6,6 +6,7 @@ If the library is missing the import of any function raises; there is no fallbac
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -24,6 +25,8 @@ EXPORTED = (
     "bcjr_code_words", "bcjr_pack_code", "bcjr_unpack_code", "bcjr_status_string",
     "bcjr_scan_segment_length", "bcjr_scan_workspace_bytes", "bcjr_forward_scan",
     "bcjr_scan_backward_workspace_bytes", "bcjr_backward_scan", "bcjr_forward_noalloc",
+    "bcjr_code_matvec", "bcjr_int4_words", "bcjr_int4_quantize", "bcjr_int4_dequantize",
+    "bcjr_int4_matvec", "bcjr_adamw_state_numel", "bcjr_adamw_step",
 )
 # Size of the fixed device array bcjr_forward_noalloc takes its workspace from.
 NOALLOC_SCRATCH_BYTES = 256 << 20
@@ -41,6 +44,18 @@ class Trellis(ctypes.Structure):
         ("bits_per_step", ctypes.c_int32),
         ("weights_per_step", ctypes.c_int32),
         ("codebook", ctypes.c_void_p),
+    ]
+
+
+class Adamw(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("seed", ctypes.c_uint64),
     ]
 
 
@@ -98,6 +113,21 @@ def lib() -> ctypes.CDLL:
     L.bcjr_scan_backward_workspace_bytes.restype = SZ
     L.bcjr_backward_scan.argtypes = [TP, P, I64, I64, F, I64, P, P, P, P, P, P, SZ, P]
     L.bcjr_backward_scan.restype = ctypes.c_int
+    L.bcjr_code_matvec.argtypes = [TP, P, I64, I64, I64, P, P, I64, I64, ctypes.c_int, P, I64, P]
+    L.bcjr_code_matvec.restype = ctypes.c_int
+    L.bcjr_int4_words.argtypes = [I64]
+    L.bcjr_int4_words.restype = I64
+    L.bcjr_int4_quantize.argtypes = [P, ctypes.c_int, I64, I64, I64, P, P, P, P]
+    L.bcjr_int4_quantize.restype = ctypes.c_int
+    L.bcjr_int4_dequantize.argtypes = [P, P, P, I64, I64, I64, P, P]
+    L.bcjr_int4_dequantize.restype = ctypes.c_int
+    L.bcjr_int4_matvec.argtypes = [P, P, P, I64, I64, I64, P, I64, I64, ctypes.c_int, P, I64, P]
+    L.bcjr_int4_matvec.restype = ctypes.c_int
+    L.bcjr_adamw_state_numel.argtypes = [P, I64]
+    L.bcjr_adamw_state_numel.restype = I64
+    L.bcjr_adamw_step.argtypes = [P, I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                  ctypes.POINTER(Adamw), P, P, P, P, P]
+    L.bcjr_adamw_step.restype = ctypes.c_int
     L.bcjr_status_string.argtypes = [ctypes.c_int]
     L.bcjr_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -500,3 +530,210 @@ def bcjr_unpack_code(code, n, k, L, codebook=None, states=None, w_hard=None):
                                     _ptr(w_hard), _stream(dev))
     _check(st, "bcjr_unpack_code")
     return states, w_hard
+
+
+# ---- products with quantised weights -------------------------------------------------------------
+
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+U8 = torch.uint8
+
+
+def _dtype_code(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _rows2(t, name, dtype, shape):
+    """t must be a matrix of this dtype and shape (None = any size) whose rows are contiguous;
+    returns the elements between its rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or any(s is not None and s != have for s, have in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride = t.stride(0) if rows > 1 else cols
+    if stride < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return stride
+
+
+def _product_io(x, y, rows):
+    """Checks x [tokens, cols] and y [tokens, rows] of a product; returns their dtype code and strides."""
+    code = _dtype_code(x, "x")
+    xs = _rows2(x, "x", x.dtype, (None, None))
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("x requires a gradient, which products with quantised weights do not give: "
+                         "call them under torch.no_grad() or on x.detach()")
+    ys = rows if y is None else _rows2(y, "y", x.dtype, (x.shape[0], rows))
+    return code, xs, ys
+
+
+def bcjr_code_matvec(x, code, codebook, n, k, L, scales=None, y=None):
+    """Products y [tokens, rows] = x [tokens, cols] W^T with trellis-coded weights: uint32 codes
+    [rows cols / L, words] of the chains cut row-major from W, optionally a fp32 scale for each."""
+    dt, xs, ys = _product_io(x, y, None)
+    tokens, cols = x.shape
+    B, nw = _chains2(code, "code", U32)
+    words = bcjr_code_words(n, k, L)
+    if words == 0 or nw != words:
+        raise ValueError(f"code has {nw} words per chain; n={n}, k={k}, L={L} need {words}")
+    if cols < 1 or cols % L or B % (cols // L):
+        raise ValueError(f"{B} chains of {L} weights are no whole rows of {cols} columns")
+    rows = B // (cols // L)
+    if y is not None:
+        ys = _rows2(y, "y", x.dtype, (tokens, rows))
+    else:
+        ys = rows
+    _spec(codebook, "codebook", F32, (1 << int(n),))
+    _spec(scales, "scales", F32, (B,))
+    dev = _device(x, code, codebook, scales, y)
+    y = torch.empty((tokens, rows), dtype=x.dtype, device=dev) if y is None else y
+    tr = trellis(n, k, codebook)
+    with torch.cuda.device(dev):
+        st = lib().bcjr_code_matvec(ctypes.byref(tr), _ptr(code), rows, cols, int(L), _ptr(scales),
+                                    _ptr(x), tokens, xs, dt, _ptr(y), ys, _stream(dev))
+    _check(st, "bcjr_code_matvec")
+    return y
+
+
+def bcjr_int4_words(cols: int) -> int:
+    return int(lib().bcjr_int4_words(int(cols)))
+
+
+def _group(group):
+    group = int(group)
+    if group < 32 or group % 32:
+        raise ValueError(f"group must be a positive multiple of 32, got {group}")
+    return group
+
+
+def bcjr_int4_quantize(w, group, with_zeros=False):
+    """4-bit codes of w [rows, cols]; returns (q uint32 [rows, words], scales fp32 [rows, groups],
+    zeros uint8 [rows, groups] or None)."""
+    dt = _dtype_code(w, "w")
+    rows, cols = _chains2(w, "w", w.dtype)
+    group = _group(group)
+    if cols < 1:
+        raise ValueError("w has no columns")
+    dev = _device(w)
+    groups = -(-cols // group)
+    q = torch.empty((rows, bcjr_int4_words(cols)), dtype=U32, device=dev)
+    scales = torch.empty((rows, groups), dtype=F32, device=dev)
+    zeros = torch.empty((rows, groups), dtype=U8, device=dev) if with_zeros else None
+    with torch.cuda.device(dev):
+        st = lib().bcjr_int4_quantize(_ptr(w), dt, rows, cols, group, _ptr(q), _ptr(scales),
+                                      _ptr(zeros), _stream(dev))
+    _check(st, "bcjr_int4_quantize")
+    return q, scales, zeros
+
+
+def _int4_weights(q, scales, zeros, cols, group):
+    """Checks 4-bit weights against their number of columns; returns their rows."""
+    rows, nw = _chains2(q, "q", U32)
+    words = bcjr_int4_words(cols)
+    if nw != words:
+        raise ValueError(f"q has {nw} words in a row; {cols} columns need {words}")
+    groups = -(-cols // group)
+    _spec(scales, "scales", F32, (rows, groups))
+    if scales is None:
+        raise ValueError("scales are required")
+    _spec(zeros, "zeros", U8, (rows, groups))
+    return rows
+
+
+def bcjr_int4_dequantize(q, scales, zeros, cols, group, w=None):
+    """The weights that 4-bit codes stand for, fp32 [rows, cols]."""
+    cols, group = int(cols), _group(group)
+    rows = _int4_weights(q, scales, zeros, cols, group)
+    _spec(w, "w", F32, (rows, cols))
+    dev = _device(q, scales, zeros, w)
+    w = torch.empty((rows, cols), dtype=F32, device=dev) if w is None else w
+    with torch.cuda.device(dev):
+        st = lib().bcjr_int4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), rows, cols, group,
+                                        _ptr(w), _stream(dev))
+    _check(st, "bcjr_int4_dequantize")
+    return w
+
+
+def bcjr_int4_matvec(x, q, scales, zeros, group, y=None):
+    """Products y [tokens, rows] = x [tokens, cols] W^T with 4-bit weights."""
+    dt, xs, _ = _product_io(x, None, 0)
+    tokens, cols = x.shape
+    group = _group(group)
+    rows = _int4_weights(q, scales, zeros, cols, group)
+    ys = rows if y is None else _rows2(y, "y", x.dtype, (tokens, rows))
+    dev = _device(x, q, scales, zeros, y)
+    y = torch.empty((tokens, rows), dtype=x.dtype, device=dev) if y is None else y
+    with torch.cuda.device(dev):
+        st = lib().bcjr_int4_matvec(_ptr(q), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(x),
+                                    tokens, xs, dt, _ptr(y), ys, _stream(dev))
+    _check(st, "bcjr_int4_matvec")
+    return y
+
+
+# ---- AdamW ---------------------------------------------------------------------------------------
+
+E4M3 = torch.float8_e4m3fn
+MOMENT_BLOCK = 32
+
+
+def bcjr_adamw_state_numel(numels) -> int:
+    """Elements of the moment arrays of tensors with these numbers of elements."""
+    return sum(-(-int(n) // MOMENT_BLOCK) * MOMENT_BLOCK for n in numels)
+
+
+def bcjr_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_scale=None, *, step,
+                    lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, seed=0):
+    """One AdamW step in place over a list of tensors. exp_avg and exp_avg_sq are the moments of all
+    of them, bcjr_adamw_state_numel() elements each: fp32, or float8_e4m3fn with the uint8 block
+    exponents avg_scale and avg_sq_scale (exp_avg_sq then holds the second moment's root)."""
+    params, grads = list(params), list(grads)
+    if len(params) != len(grads):
+        raise ValueError(f"{len(params)} params and {len(grads)} grads")
+    if not params:
+        return
+    pt, gt = _dtype_code(params[0], "params[0]"), _dtype_code(grads[0], "grads[0]")
+    pd, gd, dev = params[0].dtype, grads[0].dtype, params[0].device
+    table, total = [], 0
+    for i, (p, g) in enumerate(zip(params, grads)):
+        if not isinstance(p, torch.Tensor) or not isinstance(g, torch.Tensor):
+            raise TypeError(f"params[{i}] and grads[{i}] must be tensors")
+        if p.dtype != pd or g.dtype != gd:
+            raise ValueError(f"params[{i}] is {p.dtype} and grads[{i}] {g.dtype}, expected {pd} and {gd}")
+        if p.shape != g.shape:
+            raise ValueError(f"params[{i}] has shape {tuple(p.shape)}, its grad {tuple(g.shape)}")
+        if not (p.is_contiguous() and g.is_contiguous()):
+            raise ValueError(f"params[{i}] and grads[{i}] must be contiguous")
+        n = p.numel()
+        table += (p.data_ptr(), g.data_ptr(), n)
+        total += -(-n // MOMENT_BLOCK) * MOMENT_BLOCK
+    if exp_avg is None or exp_avg_sq is None:
+        raise ValueError("exp_avg and exp_avg_sq are required")
+    bits = 8 if isinstance(exp_avg, torch.Tensor) and exp_avg.dtype == E4M3 else 32
+    for t, name in ((exp_avg, "exp_avg"), (exp_avg_sq, "exp_avg_sq")):
+        _spec(t, name, E4M3 if bits == 8 else F32, (total,))
+    for t, name in ((avg_scale, "avg_scale"), (avg_sq_scale, "avg_sq_scale")):
+        if (t is None) != (bits == 32):
+            raise ValueError(f"{name} goes with moments in 8 bits, and only with them")
+        _spec(t, name, U8, (total // MOMENT_BLOCK,))
+    for t in (*params, *grads):
+        if t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: a call runs on one device")
+    dev = _device(params[0], exp_avg, exp_avg_sq, avg_scale, avg_sq_scale)
+    table = array.array("q", table)
+    hyper = Adamw(lr, beta1, beta2, eps, weight_decay, int(step), int(seed) & 0xFFFFFFFF)
+    with torch.cuda.device(dev):
+        st = lib().bcjr_adamw_step(table.buffer_info()[0], len(params), pt, gt, bits, ctypes.byref(hyper),
+                                   _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale),
+                                   _stream(dev))
+    _check(st, "bcjr_adamw_step")
+    # the kernel wrote behind autograd's back: a graph that saved a param must know
+    torch.autograd.graph.increment_version(params)

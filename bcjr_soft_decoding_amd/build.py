@@ -29,7 +29,8 @@ FLAGS = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 SOURCES = ["host.cpp", "sparse_kernels.hip", "viterbi_kernels.hip", "dense_kernels.hip", "code_kernels.hip",
-           "scan_kernels.hip", "noalloc.hip"]
+           "scan_kernels.hip", "noalloc.hip", "host_ops.cpp", "linear_kernels.hip", "int4_kernels.hip",
+           "optim_kernels.hip"]
 # Second translation units: (source, object name, extra options). sparse_kernels.hip is built a
 # second time with only the shapes whose fp32-message kernels run faster under the machine
 # scheduler that maximises instruction-level parallelism (see ilp_fwd_shape / ilp_bwd_shape).

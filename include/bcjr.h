@@ -336,6 +336,133 @@ bcjr_status bcjr_dense_backward(int32_t S, const float* theta, const float* code
                                 float* grad_codebook, float* grad_theta, void* ws, size_t ws_bytes,
                                 bcjr_stream_t stream);
 
+/* ---- Products with quantised weights ----------------------------------------------------------
+ * What a trained layer answers with: y = x W^T for a few tokens x, W held as the packed hard code
+ * or as 4-bit codes with a scale for each group of columns. Products are summed in fp32 and rounded
+ * once to the type of y. Tokens and output rows are independent, and a token's outputs do not
+ * depend on how many others the call holds within the types' precision (not bitwise: the tile that
+ * is used goes by the number of tokens). A NaN or Inf in x makes that token's outputs NaN or Inf
+ * (Inf may become NaN); one in a scale or in a codeword does so for the rows it scales or for every
+ * output. These calls need no workspace and may be captured into a graph.
+ */
+typedef enum { BCJR_F32 = 0, BCJR_F16 = 1, BCJR_BF16 = 2 } bcjr_dtype; /* IEEE half; bfloat16 */
+
+/*
+ * Products with trellis-coded weights: W[r, q L + t] = scales[r cols/L + q] c(s_t) with s_t the
+ * n-bit window of the chain's code that starts at bit k t (bcjr_pack_code), the chains cut row-major
+ * from W.
+ * code   DEVICE uint32 [rows cols / L, bcjr_code_words(tr, L)]; tr->codebook DEVICE [S]
+ * scales DEVICE fp32 [rows cols / L], one for each chain, or NULL (1)
+ * x      DEVICE [tokens, cols] of type dtype, rows x_stride >= cols elements apart
+ * y      DEVICE [tokens, rows] of type dtype, written, rows y_stride >= rows elements apart; what
+ *        lies between its rows is left as it was
+ * x and y are aligned to their elements (BCJR_E_ARG otherwise); x aligned to 16 bytes with an
+ * x_stride that is a multiple of 8 is read with wider loads. y may not overlap any input.
+ * Errors: BCJR_E_SHAPE (a negative size, cols < 1, L < 1 or not a divisor of cols, a stride below
+ * its row, an array beyond 2^40 elements), BCJR_E_ARG, BCJR_E_UNSUPPORTED (weights_per_step != 1).
+ * rows = 0 or tokens = 0 enqueues nothing.
+ */
+bcjr_status bcjr_code_matvec(const bcjr_trellis* tr, const uint32_t* code, int64_t rows,
+                             int64_t cols, int64_t L, const float* scales, const void* x,
+                             int64_t tokens, int64_t x_stride, bcjr_dtype dtype, void* y,
+                             int64_t y_stride, bcjr_stream_t stream);
+
+/*
+ * 4-bit weights: W[r, c] = (q[r, c] - z[r, g]) scales[r, g], g = c / group, q in 0 .. 15, and
+ * z = 8 without zero points. Layout of the codes: a row is ceil(cols / 128) blocks of 128 columns,
+ * 16 words each; word 4 g + j of a block holds its columns 32 j + 8 g .. + 7 (a lane of a 16-row
+ * matrix tile loads four words and has its operands of four products). Of a word's columns
+ * c = 0 .. 7 the even ones are the nibbles c / 2 and the odd ones the nibbles 4 + (c - 1) / 2, counted
+ * from the low end, so that shifts and masks leave neighbours in the two halves of a register.
+ * Nibbles of columns >= cols are zero.
+ */
+
+/* 32-bit words of one row of codes, 16 ceil(cols / 128); 0 for cols < 1. Host only. */
+int64_t bcjr_int4_words(int64_t cols);
+
+/*
+ * Round weights to 4 bits. Without zero points (zeros = NULL) scales = max |w| / 7 over the group and
+ * q = rint(w / scales) + 8; with them scales = (hi - lo) / 15, hi = max(w, 0), lo = min(w, 0),
+ * z = rint(-lo / scales) and q = rint(w / scales) + z, all held to their ranges. Codes go by the
+ * fp32 scale that is written, and are what exact division and rounding to nearest (ties to even)
+ * give. A group of zeros has scale 0 (and z = 0); one that holds a NaN or Inf has scale NaN and
+ * codes z (z = 0 with zero points).
+ * w      DEVICE [rows, cols] of type dtype; group: a multiple of 32 (BCJR_E_SHAPE otherwise)
+ * q      DEVICE uint32 [rows, bcjr_int4_words(cols)] written, 16-byte aligned
+ * scales DEVICE fp32 [rows, ceil(cols / group)] written;  zeros DEVICE uint8, the same, or NULL
+ */
+bcjr_status bcjr_int4_quantize(const void* w, bcjr_dtype dtype, int64_t rows, int64_t cols,
+                               int64_t group, uint32_t* q, float* scales, uint8_t* zeros,
+                               bcjr_stream_t stream);
+
+/* The weights that 4-bit codes stand for, fp32 [rows, cols], written to w. */
+bcjr_status bcjr_int4_dequantize(const uint32_t* q, const float* scales, const uint8_t* zeros,
+                                 int64_t rows, int64_t cols, int64_t group, float* w,
+                                 bcjr_stream_t stream);
+
+/*
+ * Products with 4-bit weights; x, y, strides, types and errors as in bcjr_code_matvec.
+ * q DEVICE, 16-byte aligned (BCJR_E_ARG otherwise); zeros DEVICE or NULL (z = 8; z > 15 is not
+ * checked and stands for itself).
+ */
+bcjr_status bcjr_int4_matvec(const uint32_t* q, const float* scales, const uint8_t* zeros,
+                             int64_t rows, int64_t cols, int64_t group, const void* x,
+                             int64_t tokens, int64_t x_stride, bcjr_dtype dtype, void* y,
+                             int64_t y_stride, bcjr_stream_t stream);
+
+/* ---- AdamW -----------------------------------------------------------------------------------
+ * One step over a list of tensors (Loshchilov and Hutter's decoupled weight decay):
+ *   m' = beta1 m + (1 - beta1) g                 v' = beta2 v + (1 - beta2) g^2
+ *   p' = p - lr weight_decay p - lr (m' / (1 - beta1^step)) / (sqrt(v' / (1 - beta2^step)) + eps)
+ * The moments of all tensors lie in one array each. Tensor i has the elements from
+ * first_i = sum_{j<i} 32 ceil(numel_j / 32) on; the up to 31 behind its last are neither read nor
+ * written.
+ *   state_bits = 32: exp_avg = m and exp_avg_sq = v in fp32; the scales are not used.
+ *   state_bits = 8:  blocks of 32 elements with codes in e4m3 (OCP) and one power of two each,
+ *     2^(b - 127), b the byte in avg_scale / avg_sq_scale. exp_avg holds m, exp_avg_sq holds
+ *     r = sqrt(v). b puts the block's largest finite magnitude in [128, 256) (held to 0 .. 254, 0
+ *     for a block of zeros), so nothing saturates. y = x 2^(127-b) becomes u floor(|y| / u + d)
+ *     with y's sign, u the spacing of e4m3 at y and d = (h + 1/2) / 2^16 a dither from a hash h of
+ *     the element's place, step and seed: rounding to nearest would never move r, whose change in
+ *     a step is far below u / 2. (The dither's noise on v's average over 1 / (1 - beta2) steps is about
+ *     30 % in an element, r's 15 %, and puts v's mean up to about 6 % high, whatever beta2.) r > 0 becomes at least u, so that no zero divides a moment that
+ *     lives on. This step's p' goes by the moments before their rounding. A moment that is not
+ *     finite becomes NaN, and its neighbours are unaffected. Moments are computed in fp64, since
+ *     the border of a code decides it.
+ * All zero bytes are the state before the first step, in either form.
+ */
+typedef struct {
+  void* param;      /* DEVICE [numel], updated in place */
+  const void* grad; /* DEVICE [numel] */
+  int64_t numel;    /* >= 0 */
+} bcjr_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay; /* lr, eps, weight_decay >= 0; betas in [0, 1) */
+  int64_t step;                               /* 1 for the first step */
+  uint64_t seed;                              /* of the dither; its low 32 bits are used */
+} bcjr_adamw;
+
+/* Elements of exp_avg (and of exp_avg_sq) for these tensors, sum 32 ceil(numel / 32); a scale
+ * array has 1/32 of that. 0 for a negative numel or count, a null pointer, or more than 2^40. Only
+ * numel is read. Host only. */
+int64_t bcjr_adamw_state_numel(const bcjr_adamw_tensor* tensors, int64_t count);
+
+/*
+ * tensors  host array of count entries; it may be freed when the call returns. Every param is of
+ *          param_type, every grad of grad_type, each aligned to its elements. No two params may
+ *          overlap (BCJR_E_ARG), nor a param and a grad or the state.
+ * exp_avg, exp_avg_sq  DEVICE, bcjr_adamw_state_numel() fp32 values or bytes, 16-byte aligned
+ * avg_scale, avg_sq_scale  DEVICE, bytes; NULL with state_bits = 32
+ * bf16 and fp16 params are rounded to nearest, so updates below half a spacing are lost: keep
+ * latent weights in fp32. The numbers in hyper are the call's: a captured call repeats them.
+ * Errors: BCJR_E_SHAPE (sizes), BCJR_E_ARG, BCJR_E_UNSUPPORTED (state_bits other than 8 and 32).
+ */
+bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int64_t count, bcjr_dtype param_type,
+                            bcjr_dtype grad_type, int state_bits, const bcjr_adamw* hyper,
+                            void* exp_avg, void* exp_avg_sq, uint8_t* avg_scale,
+                            uint8_t* avg_sq_scale, bcjr_stream_t stream);
+
 /* Text of a status code (static storage). */
 const char* bcjr_status_string(bcjr_status s);
 

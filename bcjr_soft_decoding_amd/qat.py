@@ -17,7 +17,10 @@ this is the per-layer reconstruction objective on synthetic calibration inputs):
 
 the squared output error per calibration sample, whose gradient per weight does not shrink
 with the layer's size (reports also give it per weight, divided by R C). The layer is cut row-major into trellis chains of L weights; the
-optimiser is plain SGD, so every coordinate moves by at most eta * g_max per step. All trellis
+optimiser is plain SGD, so every coordinate moves by at most eta * g_max per step, or AdamW
+(``optim.AdamW``, moments in fp32 or 8 bits), whose steps do not scale with the gradient. With
+``serve`` the trained layer also answers the held-out inputs from its packed code
+(``linear.CodedLinear``), next to the 4-bit round-to-nearest baseline (``linear.Int4Linear``). All trellis
 work runs in the HIP kernels (``autograd.soft_quantize`` and ``bcjr.viterbi_decode``); torch
 supplies the two matmuls of the loss and its gradient.
 
@@ -27,13 +30,17 @@ from __future__ import annotations
 
 import argparse
 import json
+import math
 import time
 from dataclasses import dataclass, field
 
 import numpy as np
 import torch
 
-from . import autograd, bcjr, synth
+from . import autograd, bcjr, linear, optim, synth
+
+
+OPTIMIZERS = ("sgd", "adamw", "adamw8")
 
 
 @dataclass
@@ -47,8 +54,12 @@ class QATConfig:
     lr: float = 1e-4       # SGD step size eta
     r_voronoi: float = 1e-3
     segmented: bool = False  # parallel-in-L entry points (for long chains, e.g. L = a whole row)
+    optimizer: str = "sgd"   # or "adamw" / "adamw8": AdamW with moments in fp32 / in 8 bits
+    betas: tuple = (0.9, 0.999)  # of AdamW, which runs without weight decay here
 
     def check(self):
+        if self.optimizer not in OPTIMIZERS:
+            raise ValueError(f"optimizer must be one of {', '.join(OPTIMIZERS)}, got {self.optimizer}")
         if self.steps < 1 or self.L < 1:
             raise ValueError("steps and L must be positive")
         if not (self.t0 > 0 and self.t_end > 0):
@@ -66,8 +77,15 @@ class QATResult:
     seconds: float = 0.0
 
     def budget(self, cfg: QATConfig) -> float:
-        """eta * N * g_max: an upper bound on drift_inf under SGD."""
-        return cfg.lr * cfg.steps * self.g_max
+        """An upper bound on drift_inf: eta * N * g_max under SGD. Under AdamW a step is at most eta
+        (1 - b1) / sqrt((1 - b2) (1 - b1^2 / b2)) (Cauchy-Schwarz on the moments' sums, for b1^2 < b2;
+        moments in 8 bits keep it but for their rounding)."""
+        if cfg.optimizer == "sgd":
+            return cfg.lr * cfg.steps * self.g_max
+        b1, b2 = cfg.betas
+        if b1 * b1 >= b2:
+            return math.inf
+        return cfg.lr * cfg.steps * (1 - b1) / math.sqrt((1 - b2) * (1 - b1 * b1 / b2))
 
 
 def temperature(cfg: QATConfig, i: int) -> float:
@@ -95,7 +113,7 @@ def step(w, W, X, codebook, cfg: QATConfig, T: float):
 
 
 def train(W, X, codebook, cfg: QATConfig, log_every: int = 0) -> QATResult:
-    """SGD on the latent weights from w = W through the annealed schedule."""
+    """cfg.optimizer on the latent weights from w = W through the annealed schedule."""
     cfg.check()
     R, C = W.shape
     if (R * C) % cfg.L:
@@ -105,6 +123,10 @@ def train(W, X, codebook, cfg: QATConfig, log_every: int = 0) -> QATResult:
             raise TypeError(f"{name} must be an fp32 CUDA tensor")
     w = W.clone()
     res = QATResult(w=w)
+    opt = None
+    if cfg.optimizer != "sgd":
+        opt = optim.AdamW([w], lr=cfg.lr, betas=cfg.betas, weight_decay=0.0,
+                          state_bits=8 if cfg.optimizer == "adamw8" else 32)
     g_max = torch.zeros((), dtype=torch.float32, device=W.device)
     torch.cuda.synchronize()
     t_start = time.perf_counter()
@@ -113,7 +135,10 @@ def train(W, X, codebook, cfg: QATConfig, log_every: int = 0) -> QATResult:
         loss, grad = step(w, W, X, codebook, cfg, T)
         g_i = grad.abs().max()
         g_max = torch.maximum(g_max, g_i)
-        w.sub_(cfg.lr * grad)
+        if opt is None:
+            w.sub_(cfg.lr * grad)
+        else:
+            opt.step([grad])
         if log_every and (i % log_every == 0 or i == cfg.steps - 1):
             res.history.append({"step": i, "T": T, "soft_loss": float(loss), "g_max": float(g_i)})
     torch.cuda.synchronize()
@@ -134,8 +159,29 @@ def synthetic_layer(rows: int, cols: int, samples: int, n: int, seed: int = 0, d
     return tuple(torch.from_numpy(a).to(device) for a in synth.qat_layer(rows, cols, samples, n, seed))
 
 
-def run(rows: int, cols: int, samples: int, cfg: QATConfig, seed: int = 0, log_every: int = 0):
+def output_loss(layer, W, X):
+    """recon_loss of a layer that answers from quantised weights: sum((layer(X) - X W^T)^2) / N."""
+    d = layer(X) - X @ W.t()
+    return (d * d).sum() / X.shape[0]
+
+
+def served(w, W, Xv, codebook, cfg: QATConfig, group: int = 128):
+    """The trained layer's held-out error (per weight) and bytes as it is served from its packed code,
+    and those of W rounded to 4 bits."""
+    coded = linear.CodedLinear.from_weights(w, codebook, cfg.n, cfg.k, cfg.L)
+    int4 = linear.Int4Linear.from_weights(W, group)
+    out = {}
+    for name, layer in (("code", coded), ("int4", int4)):
+        out[f"{name}_loss_heldout"] = float(output_loss(layer, W, Xv)) / W.numel()
+        out[f"{name}_bits_per_weight"] = 8 * layer.nbytes() / W.numel()
+    return out
+
+
+def run(rows: int, cols: int, samples: int, cfg: QATConfig, seed: int = 0, log_every: int = 0,
+        serve: bool = False, group: int = 128):
     """PTQ (Viterbi of W) against annealed QAT started from W, on one synthetic layer."""
+    if serve and (cols % cfg.L or group < 32 or group % 32):  # before the training, not after it
+        raise ValueError("serving needs whole chains of L weights in a row and groups of a multiple of 32 columns")
     W, X, Xv, c = synthetic_layer(rows, cols, samples, cfg.n, seed)
     ptq_states, ptq_w = hard(W, c, cfg)
     for T in (cfg.t0, cfg.t_end):  # untimed warm-up of both message precisions
@@ -146,7 +192,7 @@ def run(rows: int, cols: int, samples: int, cfg: QATConfig, seed: int = 0, log_e
     out = {
         "rows": rows, "cols": cols, "samples": samples, "S": 1 << cfg.n, "k": cfg.k, "L": cfg.L,
         "chains": rows * cols // cfg.L, "t0": cfg.t0, "t_end": cfg.t_end, "steps": cfg.steps,
-        "lr": cfg.lr, "seed": seed, "segmented": cfg.segmented,
+        "lr": cfg.lr, "seed": seed, "segmented": cfg.segmented, "optimizer": cfg.optimizer,
         # output error per weight: recon_loss / (R C)
         "ptq_loss_calib": float(recon_loss(ptq_w, W, X)) / (rows * cols),
         "ptq_loss_heldout": float(recon_loss(ptq_w, W, Xv)) / (rows * cols),
@@ -158,6 +204,8 @@ def run(rows: int, cols: int, samples: int, cfg: QATConfig, seed: int = 0, log_e
         "steps_per_s": cfg.steps / res.seconds,
         "state_steps_per_s": cfg.steps * rows * cols * (1 << cfg.n) / res.seconds,
     }
+    if serve:
+        out["served"] = served(res.w, W, Xv, c, cfg, group)
     if log_every:
         out["history"] = res.history
     return out
@@ -179,12 +227,17 @@ def main(argv=None):
     ap.add_argument("--log-every", type=int, default=0)
     ap.add_argument("--segmented", action="store_true",
                     help="use the parallel-in-L soft quantiser (long chains, e.g. --L = --cols)")
+    ap.add_argument("--optimizer", choices=OPTIMIZERS, default="sgd")
+    ap.add_argument("--serve", action="store_true",
+                    help="also answer the held-out inputs from the packed code and from 4-bit weights")
+    ap.add_argument("--group", type=int, default=128, help="columns of a 4-bit scale (with --serve)")
     a = ap.parse_args(argv)
     for lr in a.lr:
         for t0 in a.t0:
             cfg = QATConfig(n=a.n, k=a.k, L=a.L, t0=t0, t_end=a.t_end, steps=a.steps, lr=lr,
-                            segmented=a.segmented)
-            print(json.dumps(run(a.rows, a.cols, a.samples, cfg, a.seed, a.log_every)), flush=True)
+                            segmented=a.segmented, optimizer=a.optimizer)
+            print(json.dumps(run(a.rows, a.cols, a.samples, cfg, a.seed, a.log_every, a.serve, a.group)),
+                  flush=True)
 
 
 if __name__ == "__main__":

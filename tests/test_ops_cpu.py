@@ -203,3 +203,19 @@ def test_dithers_of_steps_and_moments_are_unrelated():
         assert abs(np.corrcoef(x, y)[0, 1]) < 5 / 256
     for x in (a, b, c):
         assert abs(x.mean() - 0.5) < 5 / np.sqrt(12 * 65536)
+
+
+def test_qat_options_are_checked_first():
+    from bcjr_soft_decoding_amd import qat
+
+    with pytest.raises(ValueError, match="optimizer"):
+        qat.QATConfig(optimizer="adam").check()
+    for kw in (dict(group=48), dict(group=0)):
+        with pytest.raises(ValueError, match="serving"):
+            qat.run(8, 512, 8, qat.QATConfig(), serve=True, **kw)
+    with pytest.raises(ValueError, match="serving"):
+        qat.run(8, 384, 8, qat.QATConfig(), serve=True)
+    res = qat.QATResult(w=None, g_max=2.0)
+    assert res.budget(qat.QATConfig(lr=0.5, steps=3)) == 3.0
+    assert res.budget(qat.QATConfig(lr=1.0, steps=2, optimizer="adamw")) == pytest.approx(2 * 0.1 / (0.001 * (1 - 0.81 / 0.999)) ** 0.5)
+    assert res.budget(qat.QATConfig(optimizer="adamw8", betas=(0.99, 0.9))) == float("inf")

@@ -166,16 +166,12 @@ namespace {
 template <class E, int F, int RT, int NT, int GS>
 int launch_tiles(Int4Args a, hipStream_t stream) {
   constexpr int kRowsOfWave = RT * 16 / F;
-  const int steps = ((a.cols + 127) / 128 + F - 1) / F;
-  const int64_t units = (a.rows + kRowsOfWave - 1) / kRowsOfWave;
-  // Waves along a row while that leaves each at least one step and the chip is not yet full: 8
-  // waves on each of 256 CUs.
-  int kw = 1;
-  while (kw < kMaxWaves && kw * 2 <= steps && units * kw < 2048) kw *= 2;
-  const int waves = kw < 4 ? 4 : kw;
-  a.kw = kw;
+  const int steps = ((a.tile.cols + 127) / 128 + F - 1) / F;
+  const int64_t units = (a.tile.rows + kRowsOfWave - 1) / kRowsOfWave;
+  const int kw = waves_along(steps, units), waves = kw < 4 ? 4 : kw;
+  a.tile.kw = kw;
   const int64_t rw = waves / kw, blocks = (units + rw - 1) / rw;
-  const int64_t tokens = (a.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
+  const int64_t tokens = (a.tile.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
   const size_t lds = (size_t)waves * RT * (16 / F) * NT * (16 / F) * sizeof(float);
   hipLaunchKernelGGL((k_int4_tiles<E, F, RT, NT, GS>), dim3(grid_of(blocks), (unsigned)tokens), dim3(64 * waves), lds,
                      stream, a);
@@ -192,14 +188,14 @@ int launch_tiles_group(const Int4Args& a, hipStream_t stream) {
 // The largest fold that the tokens leave room for and the columns fill.
 template <class E>
 int launch_tiles_any(const Int4Args& a, hipStream_t stream) {
-  const int blocks = (a.cols + 127) / 128;
+  const int blocks = (a.tile.cols + 127) / 128;
   if constexpr (TileOf<E>::T::kParts == 1) {
-    if (a.tokens == 1 && blocks > 8) return launch_tiles_group<E, 16, 4, 1>(a, stream);
-    if (a.tokens <= 2 && blocks > 4) return launch_tiles_group<E, 8, 4, 1>(a, stream);
+    if (a.tile.tokens == 1 && blocks > 8) return launch_tiles_group<E, 16, 4, 1>(a, stream);
+    if (a.tile.tokens <= 2 && blocks > 4) return launch_tiles_group<E, 8, 4, 1>(a, stream);
   }
-  if (a.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_group<E, 4, 2, 1>(a, stream);
-  if (a.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_group<E, 2, 2, 1>(a, stream);
-  if (a.tokens <= tile_tokens<E, 1>()) return launch_tiles_group<E, 1, 1, 1>(a, stream);
+  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_group<E, 4, 2, 1>(a, stream);
+  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_group<E, 2, 2, 1>(a, stream);
+  if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_group<E, 1, 1, 1>(a, stream);
   return launch_tiles_group<E, 1, 2, 2>(a, stream);
 }
 
@@ -216,19 +212,11 @@ int launch_int4_matvec(const uint32_t* q, const float* scales, const uint8_t* ze
     a.q = q;
     a.scales = scales;
     a.zeros = zeros;
-    a.rows = rows;
-    a.tokens = io.tokens;
-    a.xs = io.x_stride;
-    a.ys = io.y_stride;
-    a.x = io.x;
-    a.y = io.y;
-    a.cols = (int)cols;
+    a.tile = tile_args(io, rows, cols);
     a.groups = (int)groups;
     a.words = (int)bcjr_int4_words(cols);
     a.per_group = (unsigned)per_group;
     a.magic = (unsigned)((((int64_t)1 << 32) + per_group - 1) / per_group);
-    const int size = io.dtype == BCJR_F32 ? 4 : 2;
-    a.wide = (uintptr_t)io.x % 16 == 0 && io.x_stride * size % 16 == 0;
     return with_type(io.dtype, [&](auto e) {
       return launch_tiles_any<decltype(e)>(a, static_cast<hipStream_t>(stream));
     });

@@ -4,6 +4,7 @@
 // c(s_t) x[m, q L + t].
 #include <hip/hip_runtime.h>
 
+#include "code_mfma.h"
 #include "internal.h"
 #include "ops.h"
 #include "ops_device.h"
@@ -45,10 +46,72 @@ k_code_matvec(const unsigned* __restrict__ code, long long rows, long long cols,
   }
 }
 
+template <class E, int F, int RT, int NT, int K>
+int launch_tiles(CodeArgs a, hipStream_t stream) {
+  constexpr int kRowsOfWave = RT * 16 / F;
+  const int steps = (a.tile.cols / 128 + F - 1) / F;
+  const int64_t units = (a.tile.rows + kRowsOfWave - 1) / kRowsOfWave;
+  const int kw = waves_along(steps, units);
+  a.tile.kw = kw;
+  // every block makes a table: all 8 waves share it, and no more blocks than fit the chip are started
+  const int64_t rw = kMaxWaves / kw, blocks = (units + rw - 1) / rw;
+  const int64_t tokens = (a.tile.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
+  const size_t lds = (((size_t)1 << a.n) + (size_t)kMaxWaves * RT * (16 / F) * NT * (16 / F)) * sizeof(float);
+  const void* kernel = reinterpret_cast<const void*>(k_code_tiles<E, F, RT, NT, K>);
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return (int)e;
+  }
+  const int64_t room = 256 * (lds > 81920 ? 1 : 2);
+  hipLaunchKernelGGL((k_code_tiles<E, F, RT, NT, K>), dim3((unsigned)(blocks < room ? blocks : room), (unsigned)tokens),
+                     dim3(64 * kMaxWaves), lds, stream, a);
+  return (int)hipGetLastError();
+}
+
+template <class E, int F, int RT, int NT>
+int launch_tiles_bits(const CodeArgs& a, int k, hipStream_t stream) {
+  return k == 1   ? launch_tiles<E, F, RT, NT, 1>(a, stream)
+         : k == 2 ? launch_tiles<E, F, RT, NT, 2>(a, stream)
+         : k == 3 ? launch_tiles<E, F, RT, NT, 3>(a, stream)
+                  : launch_tiles<E, F, RT, NT, 4>(a, stream);
+}
+
+// The largest fold that the tokens leave room for and the columns fill.
+template <class E>
+int launch_tiles_any(const CodeArgs& a, int k, hipStream_t stream) {
+  const int blocks = a.tile.cols / 128;
+  if constexpr (TileOf<E>::T::kParts == 1) {
+    if (a.tile.tokens == 1 && blocks > 8) return launch_tiles_bits<E, 16, 2, 1>(a, k, stream);
+    if (a.tile.tokens <= 2 && blocks > 4) return launch_tiles_bits<E, 8, 2, 1>(a, k, stream);
+  }
+  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_bits<E, 4, 2, 1>(a, k, stream);
+  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_bits<E, 2, 1, 1>(a, k, stream);
+  if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_bits<E, 1, 1, 1>(a, k, stream);
+  return launch_tiles_bits<E, 1, 1, 2>(a, k, stream);
+}
+
 }  // namespace
 
 int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t cols, int64_t L,
                        const float* codebook, const float* scales, const MatvecIO& io, void* stream) {
+  // The matrix-core form: whole blocks of 128 columns in a chain, a table that fits LDS, offsets in
+  // 32 bits, and a block's chain from one high product, exact while (blocks + 16) per_chain < 2^32.
+  const int64_t per_chain = L / 128, words = code_words(n, k, L);
+  if (L % 128 == 0 && n <= 15 && k <= 4 && cols <= ((int64_t)1 << 20) && io.tokens <= 65535) {
+    CodeArgs a;
+    a.tile = tile_args(io, rows, cols);
+    a.code = code;
+    a.codebook = codebook;
+    a.scales = scales;
+    a.n = n;
+    a.chains = (int)(cols / L);
+    a.words = (int)words;
+    a.per_chain = (unsigned)per_chain;
+    a.magic = (unsigned)((((int64_t)1 << 32) + per_chain - 1) / per_chain);
+    return with_type(io.dtype, [&](auto e) {
+      return launch_tiles_any<decltype(e)>(a, k, static_cast<hipStream_t>(stream));
+    });
+  }
   return with_type(io.dtype, [&](auto e) {
     using E = decltype(e);
     const int64_t blocks = (io.tokens + 3) / 4;

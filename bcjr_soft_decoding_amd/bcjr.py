@@ -142,8 +142,31 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of current_stream()'s time
+
+
 def _stream(device):
+    if _raw_stream is not None and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+class _NoSwitch:
+    """The context of a call whose device is the current one already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(device):
+    """The context that a call on this device is made in."""
+    return _NO_SWITCH if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def trellis(n: int, k: int, codebook=None, v: int = 1) -> Trellis:
@@ -168,6 +191,8 @@ F32, I32, U32 = torch.float32, torch.int32, torch.uint32
 def _spec(t, name, dtype, shape):
     """t (None = not given) must be a contiguous tensor of this dtype and exact shape."""
     if t is None:
+        return
+    if type(t) is torch.Tensor and t.dtype == dtype and (shape is None or t.shape == shape) and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -557,6 +582,8 @@ def _rows2(t, name, dtype, shape):
     if t.dim() != 2 or any(s is not None and s != have for s, have in zip(shape, t.shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     rows, cols = t.shape
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
     stride = t.stride(0) if rows > 1 else cols
@@ -565,41 +592,49 @@ def _rows2(t, name, dtype, shape):
     return stride
 
 
-def _product_io(x, y, rows):
-    """Checks x [tokens, cols] and y [tokens, rows] of a product; returns their dtype code and strides."""
+def _product_x(x):
+    """Checks the x [tokens, cols] of a product; returns its dtype code, tokens, columns and row stride."""
     code = _dtype_code(x, "x")
-    xs = _rows2(x, "x", x.dtype, (None, None))
+    stride = _rows2(x, "x", x.dtype, (None, None))
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("x requires a gradient, which products with quantised weights do not give: "
                          "call them under torch.no_grad() or on x.detach()")
-    ys = rows if y is None else _rows2(y, "y", x.dtype, (x.shape[0], rows))
-    return code, xs, ys
+    tokens, cols = x.shape
+    return code, tokens, cols, stride
+
+
+def _product_y(x, y, tokens, rows, dev):
+    """The output of a product and its row stride: the caller's, checked, or a new one."""
+    if y is None:
+        return x.new_empty((tokens, rows)), rows
+    if y.device != dev:
+        raise ValueError(f"tensors on {dev} and {y.device}: a call runs on one device")
+    return y, _rows2(y, "y", x.dtype, (tokens, rows))
 
 
 def bcjr_code_matvec(x, code, codebook, n, k, L, scales=None, y=None):
     """Products y [tokens, rows] = x [tokens, cols] W^T with trellis-coded weights: uint32 codes
     [rows cols / L, words] of the chains cut row-major from W, optionally a fp32 scale for each."""
-    dt, xs, ys = _product_io(x, y, None)
-    tokens, cols = x.shape
+    dt, tokens, cols, xs = _product_x(x)
     B, nw = _chains2(code, "code", U32)
-    words = bcjr_code_words(n, k, L)
+    n, k, L = int(n), int(k), int(L)
+    words = (n + k * (L - 1) + 31) // 32 if L > 0 and 1 <= k <= n <= 16 else 0
     if words == 0 or nw != words:
         raise ValueError(f"code has {nw} words per chain; n={n}, k={k}, L={L} need {words}")
     if cols < 1 or cols % L or B % (cols // L):
         raise ValueError(f"{B} chains of {L} weights are no whole rows of {cols} columns")
     rows = B // (cols // L)
-    if y is not None:
-        ys = _rows2(y, "y", x.dtype, (tokens, rows))
-    else:
-        ys = rows
-    _spec(codebook, "codebook", F32, (1 << int(n),))
+    _spec(codebook, "codebook", F32, (1 << n,))
     _spec(scales, "scales", F32, (B,))
-    dev = _device(x, code, codebook, scales, y)
-    y = torch.empty((tokens, rows), dtype=x.dtype, device=dev) if y is None else y
-    tr = trellis(n, k, codebook)
-    with torch.cuda.device(dev):
-        st = lib().bcjr_code_matvec(ctypes.byref(tr), _ptr(code), rows, cols, int(L), _ptr(scales),
-                                    _ptr(x), tokens, xs, dt, _ptr(y), ys, _stream(dev))
+    if y is not None:
+        _rows2(y, "y", x.dtype, (tokens, rows))
+    dev = _device(x, code, codebook, scales)
+    y, ys = _product_y(x, y, tokens, rows, dev)
+    tr = Trellis(n, k, 1, codebook.data_ptr())
+    with _on(dev):
+        st = lib().bcjr_code_matvec(ctypes.byref(tr), code.data_ptr(), rows, cols, L,
+                                    None if scales is None else scales.data_ptr(), x.data_ptr(), tokens, xs, dt,
+                                    y.data_ptr(), ys, _stream(dev))
     _check(st, "bcjr_code_matvec")
     return y
 
@@ -628,7 +663,7 @@ def bcjr_int4_quantize(w, group, with_zeros=False):
     q = torch.empty((rows, bcjr_int4_words(cols)), dtype=U32, device=dev)
     scales = torch.empty((rows, groups), dtype=F32, device=dev)
     zeros = torch.empty((rows, groups), dtype=U8, device=dev) if with_zeros else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().bcjr_int4_quantize(_ptr(w), dt, rows, cols, group, _ptr(q), _ptr(scales),
                                       _ptr(zeros), _stream(dev))
     _check(st, "bcjr_int4_quantize")
@@ -656,7 +691,7 @@ def bcjr_int4_dequantize(q, scales, zeros, cols, group, w=None):
     _spec(w, "w", F32, (rows, cols))
     dev = _device(q, scales, zeros, w)
     w = torch.empty((rows, cols), dtype=F32, device=dev) if w is None else w
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().bcjr_int4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), rows, cols, group,
                                         _ptr(w), _stream(dev))
     _check(st, "bcjr_int4_dequantize")
@@ -665,16 +700,16 @@ def bcjr_int4_dequantize(q, scales, zeros, cols, group, w=None):
 
 def bcjr_int4_matvec(x, q, scales, zeros, group, y=None):
     """Products y [tokens, rows] = x [tokens, cols] W^T with 4-bit weights."""
-    dt, xs, _ = _product_io(x, None, 0)
-    tokens, cols = x.shape
+    dt, tokens, cols, xs = _product_x(x)
     group = _group(group)
     rows = _int4_weights(q, scales, zeros, cols, group)
-    ys = rows if y is None else _rows2(y, "y", x.dtype, (tokens, rows))
-    dev = _device(x, q, scales, zeros, y)
-    y = torch.empty((tokens, rows), dtype=x.dtype, device=dev) if y is None else y
-    with torch.cuda.device(dev):
-        st = lib().bcjr_int4_matvec(_ptr(q), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(x),
-                                    tokens, xs, dt, _ptr(y), ys, _stream(dev))
+    if y is not None:
+        _rows2(y, "y", x.dtype, (tokens, rows))
+    dev = _device(x, q, scales, zeros)
+    y, ys = _product_y(x, y, tokens, rows, dev)
+    with _on(dev):
+        st = lib().bcjr_int4_matvec(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                                    rows, cols, group, x.data_ptr(), tokens, xs, dt, y.data_ptr(), ys, _stream(dev))
     _check(st, "bcjr_int4_matvec")
     return y
 
@@ -712,6 +747,8 @@ def bcjr_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_s
             raise ValueError(f"params[{i}] has shape {tuple(p.shape)}, its grad {tuple(g.shape)}")
         if not (p.is_contiguous() and g.is_contiguous()):
             raise ValueError(f"params[{i}] and grads[{i}] must be contiguous")
+        if p.device != dev or g.device != dev:
+            raise ValueError(f"tensors on {dev}, {p.device} and {g.device}: a call runs on one device")
         n = p.numel()
         table += (p.data_ptr(), g.data_ptr(), n)
         total += -(-n // MOMENT_BLOCK) * MOMENT_BLOCK
@@ -724,16 +761,14 @@ def bcjr_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_s
         if (t is None) != (bits == 32):
             raise ValueError(f"{name} goes with moments in 8 bits, and only with them")
         _spec(t, name, U8, (total // MOMENT_BLOCK,))
-    for t in (*params, *grads):
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: a call runs on one device")
     dev = _device(params[0], exp_avg, exp_avg_sq, avg_scale, avg_sq_scale)
     table = array.array("q", table)
     hyper = Adamw(lr, beta1, beta2, eps, weight_decay, int(step), int(seed) & 0xFFFFFFFF)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().bcjr_adamw_step(table.buffer_info()[0], len(params), pt, gt, bits, ctypes.byref(hyper),
-                                   _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale),
-                                   _stream(dev))
+                                   exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
+                                   None if avg_scale is None else avg_scale.data_ptr(),
+                                   None if avg_sq_scale is None else avg_sq_scale.data_ptr(), _stream(dev))
     _check(st, "bcjr_adamw_step")
     # the kernel wrote behind autograd's back: a graph that saved a param must know
     torch.autograd.graph.increment_version(params)

@@ -18,7 +18,8 @@ struct CodeArgs {
   const float* codebook;
   const float* scales;         // of a chain, or NULL
   int n, chains, words;        // state bits; chains of a row; words of a chain
-  unsigned per_chain, magic;   // blocks of 128 columns in a chain; ceil(2^32 / per_chain) for > 1
+  int per_chain;               // blocks of 128 columns in a chain
+  float reciprocal;            // 1 / per_chain
 };
 
 namespace {
@@ -145,11 +146,10 @@ k_code_tiles(const CodeArgs a) {
       for (int u = 0; u < kKept; ++u) so[t][u] = (unsigned)(min(t * kRows + pl.sum_row(u), last) * a.chains);
     }
     for (int s = ki; s < steps; s += kw) {
-      const unsigned block = (unsigned)(s * F + pl.fold);
-      const bool in = (int)block < blocks;
-      unsigned chain = a.per_chain == 1 ? block : __umulhi(block, a.magic);
+      const int block = s * F + pl.fold;
+      const bool in = block < blocks;
+      const int chain = min(divide(block, a.reciprocal), a.chains - 1);
       const unsigned at = chain * a.words + (block - chain * a.per_chain) * (4 * K);
-      chain = min(chain, (unsigned)(a.chains - 1));
       unsigned w[RT][K + 1];
 #pragma unroll
       for (int t = 0; t < RT; ++t)
@@ -161,7 +161,7 @@ k_code_tiles(const CodeArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[n][j] = none;
-          if (in) x[n][j] = load_x8<E>(xr[n], block * 128 + 32 * pl.g + 8 * j, a.tile.cols, a.tile.wide, pl.x_part());
+          if (in) x[n][j] = load_x8<E>(xr[n], block * 128 + 32 * pl.g + 8 * j, a.tile.cols, pl.x_part());
         }
 #pragma unroll
       for (int t = 0; t < RT; ++t) {

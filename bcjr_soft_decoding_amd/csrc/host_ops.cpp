@@ -12,6 +12,7 @@ using namespace bcjr;
 namespace {
 
 constexpr int64_t kMaxElements = (int64_t)1 << 40;
+constexpr int64_t kInt4Columns = (int64_t)1 << 24;  // the kernels hold columns in 32 bits (tiles.h)
 
 bool dtype_ok(int t) { return t == BCJR_F32 || t == BCJR_F16 || t == BCJR_BF16; }
 int dtype_size(int t) { return t == BCJR_F32 ? 4 : 2; }
@@ -32,7 +33,7 @@ bool product_pointers_ok(const MatvecIO& io) {
 }
 
 bool int4_shapes_ok(int64_t rows, int64_t cols, int64_t group) {
-  return rows >= 0 && cols >= 1 && rows <= kMaxElements && cols <= kMaxElements && fits(rows, cols) &&
+  return rows >= 0 && cols >= 1 && rows <= kMaxElements && cols <= kInt4Columns && fits(rows, cols) &&
          group >= 32 && group % 32 == 0 && group <= kMaxElements;
 }
 
@@ -86,7 +87,7 @@ bcjr_status bcjr_code_matvec(const bcjr_trellis* tr, const uint32_t* code, int64
 }
 
 int64_t bcjr_int4_words(int64_t cols) {
-  return cols < 1 || cols > kMaxElements ? 0 : (cols + 127) / 128 * 16;
+  return cols < 1 || cols > kInt4Columns ? 0 : (cols + 127) / 128 * 16;
 }
 
 bcjr_status bcjr_int4_quantize(const void* w, bcjr_dtype dtype, int64_t rows, int64_t cols,

@@ -15,7 +15,7 @@ struct Int4Args {
   const float* scales;
   const uint8_t* zeros;
   int groups, words;
-  unsigned per_group, magic;  // units of 32 columns in a group; ceil(2^32 / per_group) for > 1
+  float per_group;  // 1 / (units of 32 columns in a group)
 };
 
 namespace {
@@ -80,13 +80,11 @@ k_int4_tiles(const Int4Args a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[n][j] = none;
-          if (in) x[n][j] = load_x8<E>(xr[n], block * 128 + 32 * j + 8 * pl.g, a.tile.cols, a.tile.wide, pl.x_part());
+          if (in) x[n][j] = load_x8<E>(xr[n], block * 128 + 32 * j + 8 * pl.g, a.tile.cols, pl.x_part());
         }
 #pragma unroll
       for (int j0 = 0; j0 < 4; j0 += GS) {
-        const unsigned unit = (unsigned)block * 4 + j0;
-        int group = (int)(a.per_group == 1 ? unit : __umulhi(unit, a.magic));
-        group = group < a.groups ? group : a.groups - 1;
+        const int group = min(divide(block * 4 + j0, a.per_group), a.groups - 1);
         f32x4 sum[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {

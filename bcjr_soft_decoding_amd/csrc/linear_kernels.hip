@@ -94,22 +94,23 @@ int launch_tiles_any(const CodeArgs& a, int k, hipStream_t stream) {
 
 int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t cols, int64_t L,
                        const float* codebook, const float* scales, const MatvecIO& io, void* stream) {
-  // The matrix-core form: whole blocks of 128 columns in a chain, a table that fits LDS, offsets in
-  // 32 bits, and a block's chain from one high product, exact while (blocks + 16) per_chain < 2^32.
-  const int64_t per_chain = L / 128, words = code_words(n, k, L);
-  if (L % 128 == 0 && n <= 15 && k <= 4 && cols <= ((int64_t)1 << 20) && io.tokens <= 65535) {
+  // The matrix-core form: whole blocks of 128 columns in a chain and a table that fits LDS.
+  const int64_t words = code_words(n, k, L);
+  if (L % 128 == 0 && n <= 15 && k <= 4 && cols <= kTileColumns) {
     CodeArgs a;
-    a.tile = tile_args(io, rows, cols);
     a.code = code;
     a.codebook = codebook;
     a.scales = scales;
     a.n = n;
     a.chains = (int)(cols / L);
     a.words = (int)words;
-    a.per_chain = (unsigned)per_chain;
-    a.magic = (unsigned)((((int64_t)1 << 32) + per_chain - 1) / per_chain);
-    return with_type(io.dtype, [&](auto e) {
-      return launch_tiles_any<decltype(e)>(a, k, static_cast<hipStream_t>(stream));
+    a.per_chain = (int)(L / 128);
+    a.reciprocal = 1.0f / (float)a.per_chain;
+    return in_pieces(io, io.dtype == BCJR_F32 ? 4 : 2, [&](const MatvecIO& piece) {
+      a.tile = tile_args(piece, rows, cols);
+      return with_type(io.dtype, [&](auto e) {
+        return launch_tiles_any<decltype(e)>(a, k, static_cast<hipStream_t>(stream));
+      });
     });
   }
   return with_type(io.dtype, [&](auto e) {
@@ -118,7 +119,7 @@ int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t
     const dim3 grid(grid_of((rows + 3) / 4), (unsigned)(blocks < 32768 ? blocks : 32768));
     hipLaunchKernelGGL((k_code_matvec<E, 4>), grid, dim3(256), 0, static_cast<hipStream_t>(stream),
                        code, (long long)rows, (long long)cols, (long long)L, n, k,
-                       (long long)code_words(n, k, L), codebook, scales,
+                       (long long)words, codebook, scales,
                        static_cast<const typename E::T*>(io.x), (long long)io.tokens,
                        (long long)io.x_stride, static_cast<typename E::T*>(io.y),
                        (long long)io.y_stride);

@@ -23,8 +23,7 @@ struct TileArgs {
   void* y;
   long long rows, tokens, xs, ys;
   int cols;
-  int kw;    // waves of a block that share a row, each with every kw-th step
-  int wide;  // rows of x are aligned to 16 bytes
+  int kw;  // waves of a block that share a row, each with every kw-th step
 };
 
 namespace {
@@ -62,21 +61,28 @@ __device__ inline unsigned part_of(float x, int part) {
   return __float_as_uint(part == 0 ? hi : part == 1 ? mid : r - mid) >> 16;
 }
 
+// Vectors at any element's address: the memory system splits what crosses a line, so x needs no alignment
+// and no second path.
+template <class T, int N> struct Loose;
+template <class T> struct Loose<T, 8> { typedef T V __attribute__((ext_vector_type(8), aligned(sizeof(T)))); };
+template <class T> struct Loose<T, 4> { typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T)))); };
+
 // x[col .. col + 7] as an operand, zeros from cols on.
 template <class E>
-__device__ inline typename TileOf<E>::T::V load_x8(const typename E::T* row, int col, int cols, int wide, int part) {
+__device__ inline typename TileOf<E>::T::V load_x8(const typename E::T* row, int col, int cols, int part) {
   using V = typename TileOf<E>::T::V;
-  const typename E::T* p = row + col;
+  using X = typename E::T;
+  const X* p = row + col;
   if constexpr (TileOf<E>::T::kParts == 1) {
-    if (wide && col + 8 <= cols) return *reinterpret_cast<const V*>(p);
+    if (col + 8 <= cols) return *reinterpret_cast<const typename Loose<X, 8>::V*>(p);
     V v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? p[i] : (typename E::T)0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? p[i] : (X)0.0f;
     return v;
   } else {
     float f[8];
-    if (wide && col + 8 <= cols) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+    if (col + 8 <= cols) {
+      const auto a = *reinterpret_cast<const Loose<float, 4>::V*>(p), b = *reinterpret_cast<const Loose<float, 4>::V*>(p + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
     } else {
@@ -89,6 +95,10 @@ __device__ inline typename TileOf<E>::T::V load_x8(const typename E::T* row, int
     return __builtin_bit_cast(V, v);
   }
 }
+
+// floor(u / d) for u < 2^21 from the fp32 reciprocal of d: u + 1/2 is exact, and (u + 1/2) / d is at least 1 /
+// (2 d) off any whole number, more than the two roundings' u / d 2^-23.
+__device__ inline int divide(int u, float reciprocal) { return (int)(((float)u + 0.5f) * reciprocal); }
 
 // Tokens of a tile: 16 columns are parts times folds times tokens.
 template <class E, int F>
@@ -192,9 +202,11 @@ inline int waves_along(int steps, int64_t units) {
   return kw;
 }
 
+// Products in tiles: columns are 32-bit numbers below 2^24 (divide()).
+constexpr int64_t kTileColumns = (int64_t)1 << 24;
+
 inline TileArgs tile_args(const MatvecIO& io, int64_t rows, int64_t cols) {
   TileArgs t;
-  const int size = io.dtype == BCJR_F32 ? 4 : 2;
   t.x = io.x;
   t.y = io.y;
   t.rows = rows;
@@ -203,8 +215,21 @@ inline TileArgs tile_args(const MatvecIO& io, int64_t rows, int64_t cols) {
   t.ys = io.y_stride;
   t.cols = (int)cols;
   t.kw = 1;
-  t.wide = (uintptr_t)io.x % 16 == 0 && io.x_stride * size % 16 == 0;
   return t;
+}
+
+// Calls f with the tokens in pieces that one launch's grid holds: 32768 tiles of at least 5.
+template <class Fn>
+inline int in_pieces(MatvecIO io, int dtype_size, Fn f) {
+  const int64_t most = 5 * 32768, total = io.tokens;
+  for (int64_t m = 0; m < total; m += most) {
+    MatvecIO p = io;
+    p.tokens = total - m < most ? total - m : most;
+    p.x = static_cast<const char*>(io.x) + m * io.x_stride * dtype_size;
+    p.y = static_cast<char*>(io.y) + m * io.y_stride * dtype_size;
+    if (const int e = f(p)) return e;
+  }
+  return 0;
 }
 
 }  // namespace bcjr

@@ -356,8 +356,7 @@ typedef enum { BCJR_F32 = 0, BCJR_F16 = 1, BCJR_BF16 = 2 } bcjr_dtype; /* IEEE h
  * x      DEVICE [tokens, cols] of type dtype, rows x_stride >= cols elements apart
  * y      DEVICE [tokens, rows] of type dtype, written, rows y_stride >= rows elements apart; what
  *        lies between its rows is left as it was
- * x and y are aligned to their elements (BCJR_E_ARG otherwise); x aligned to 16 bytes with an
- * x_stride that is a multiple of 8 is read with wider loads. y may not overlap any input.
+ * x and y are aligned to their elements (BCJR_E_ARG otherwise). y may not overlap any input.
  * Errors: BCJR_E_SHAPE (a negative size, cols < 1, L < 1 or not a divisor of cols, a stride below
  * its row, an array beyond 2^40 elements), BCJR_E_ARG, BCJR_E_UNSUPPORTED (weights_per_step != 1).
  * rows = 0 or tokens = 0 enqueues nothing.
@@ -374,10 +373,10 @@ bcjr_status bcjr_code_matvec(const bcjr_trellis* tr, const uint32_t* code, int64
  * matrix tile loads four words and has its operands of four products). Of a word's columns
  * c = 0 .. 7 the even ones are the nibbles c / 2 and the odd ones the nibbles 4 + (c - 1) / 2, counted
  * from the low end, so that shifts and masks leave neighbours in the two halves of a register.
- * Nibbles of columns >= cols are zero.
+ * Nibbles of columns >= cols are zero. A row has at most 2^24 columns (BCJR_E_SHAPE beyond).
  */
 
-/* 32-bit words of one row of codes, 16 ceil(cols / 128); 0 for cols < 1. Host only. */
+/* 32-bit words of one row of codes, 16 ceil(cols / 128); 0 for cols outside [1, 2^24]. Host only. */
 int64_t bcjr_int4_words(int64_t cols);
 
 /*

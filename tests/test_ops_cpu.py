@@ -64,7 +64,8 @@ def test_int4_quantize_refusals(lib):
         assert call(**kw) == want, kw
     assert lib.bcjr_int4_dequantize(P(0x1000), P(0), None, 1, 1, 32, P(0x2000), None) == ARG
     assert lib.bcjr_int4_dequantize(P(0x1000), P(0x2000), None, 1, 0, 32, P(0x2000), None) == SHAPE
-    assert [lib.bcjr_int4_words(c) for c in (-1, 0, 1, 128, 129)] == [0, 0, 16, 16, 32]
+    assert [lib.bcjr_int4_words(c) for c in (-1, 0, 1, 128, 129, 1 << 24, (1 << 24) + 1)] == [0, 0, 16, 16, 32, 1 << 21, 0]
+    assert call(cols=(1 << 24) + 1) == SHAPE and _int4(lib, cols=(1 << 24) + 1, xs=1 << 25) == SHAPE
 
 
 class Tensor(ctypes.Structure):

@@ -54,8 +54,8 @@ __device__ inline f32x4 add_products(const unsigned (&e)[8], typename T::V x, f3
       hi[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x07060302);
       lo[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x05040100);
     }
-    d = T::mfma(__builtin_bit_cast(typename T::V, lo), x, d);
-    return T::mfma(__builtin_bit_cast(typename T::V, hi), x, d);
+    d = T::mfma(x, __builtin_bit_cast(typename T::V, lo), d);
+    return T::mfma(x, __builtin_bit_cast(typename T::V, hi), d);
   } else {
     u32x4 p[3];
 #pragma unroll
@@ -74,7 +74,7 @@ __device__ inline f32x4 add_products(const unsigned (&e)[8], typename T::V x, f3
       p[2][i] = __builtin_amdgcn_perm(__float_as_uint(r[1]), __float_as_uint(r[0]), 0x07060302);
     }
 #pragma unroll
-    for (int i = 2; i >= 0; --i) d = T::mfma(__builtin_bit_cast(typename T::V, p[i]), x, d);
+    for (int i = 2; i >= 0; --i) d = T::mfma(x, __builtin_bit_cast(typename T::V, p[i]), d);
     return d;
   }
 }
@@ -108,12 +108,12 @@ k_code_tiles(const CodeArgs a) {
   constexpr int kRows = Pl::kRows, kKept = Pl::kKept;
   constexpr int kParts = std::is_same<E, F32>::value ? 3 : 2;
   constexpr int kShare = K <= 2 ? 8 : 4;  // states read from one 32-bit window: n + K (kShare - 1) <= 29
-  extern __shared__ float lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int states = 1 << a.n;
-  unsigned* table = reinterpret_cast<unsigned*>(lds);
-  float* part_sums = lds + states;
   const Pl pl;
-  const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(part_sums));
+  char* mine = lds + pl.wave * NT * kXBytes;
+  unsigned* table = reinterpret_cast<unsigned*>(lds + pl.waves * NT * kXBytes);
+  const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(lds));
   const float down = ldexpf(1.0f, -top), up = ldexpf(1.0f, top);
   for (int i = threadIdx.x; i < states; i += blockDim.x) table[i] = Codeword<E>::entry(a.codebook[i], down);
   __syncthreads();
@@ -122,10 +122,9 @@ k_code_tiles(const CodeArgs a) {
   const int blocks = a.tile.cols / 128, steps = (blocks + F - 1) / F;
   const long long rows = a.tile.rows, units = (rows + RT * kRows - 1) / (RT * kRows);  // of rows, one for a wave
   const long long m0 = (long long)blockIdx.y * (NT * Pl::kTokens);
-  const typename E::T* xr[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) xr[n] = pl.x_row(a.tile, m0, n);
-  const V none = __builtin_bit_cast(V, u32x4{0, 0, 0, 0});
+  using X = XTile<E, F, NT>;
+  X x;
+  x.init(a.tile, m0);
   const unsigned mask = (unsigned)(states - 1) << 2;
   const int shift = 30 - a.n;  // a state at the top of a window as the byte offset of its codeword
   const int more = a.n > K;    // the last of the K + 1 words is there
@@ -137,13 +136,12 @@ k_code_tiles(const CodeArgs a) {
     const int last = (int)(rows - 1 - base < RT * kRows ? rows - 1 - base : RT * kRows);
     const unsigned* __restrict__ code = a.code + base * a.chains * a.words;
     const float* __restrict__ scales = a.scales + base * a.chains;
-    unsigned co[RT], so[RT][kKept];
+    unsigned co[RT], so[RT];
     float acc[RT][NT][kKept] = {};
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      co[t] = (unsigned)(min(t * kRows + pl.weight_row(), last) * a.chains * a.words + K * pl.g);
-#pragma unroll
-      for (int u = 0; u < kKept; ++u) so[t][u] = (unsigned)(min(t * kRows + pl.sum_row(u), last) * a.chains);
+      so[t] = (unsigned)(min(t * kRows + pl.row(), last) * a.chains);
+      co[t] = so[t] * a.words + K * pl.g;
     }
     for (int s = ki; s < steps; s += kw) {
       const int block = s * F + pl.fold;
@@ -155,14 +153,14 @@ k_code_tiles(const CodeArgs a) {
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int i = 0; i <= K; ++i) w[t][i] = in && (i < K || more) ? code[co[t] + at + i] : 0u;
-      V x[NT][4];
+      x.load(a.tile, s);
+      x.put(mine);
+      V xo[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[n][j] = none;
-          if (in) x[n][j] = load_x8<E>(xr[n], block * 128 + 32 * pl.g + 8 * j, a.tile.cols, pl.x_part());
-        }
+        for (int j = 0; j < 4; ++j) xo[n][j] = X::get(mine, pl, n, 4 * pl.g + j);
+      X::in_order();
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         f32x4 d[NT];
@@ -179,14 +177,13 @@ k_code_tiles(const CodeArgs a) {
             e[i] = *reinterpret_cast<const unsigned*>(reinterpret_cast<const char*>(table) + byte);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) d[n] = add_products<T, kParts>(e, x[n][j], d[n]);
+          for (int n = 0; n < NT; ++n) d[n] = add_products<T, kParts>(e, xo[n][j], d[n]);
         }
+        const float sc = a.scales != nullptr ? scales[so[t] + chain] : 1.0f;
 #pragma unroll
-        for (int u = 0; u < kKept; ++u) {
-          const float sc = a.scales != nullptr ? scales[so[t][u] + chain] : 1.0f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[t][n][u] = fmaf(sc, pl.kept(d[n], u), acc[t][n][u]);
-        }
+          for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(sc, pl.kept(d[n], u), acc[t][n][u]);
       }
     }
     if constexpr (std::is_same<E, F16>::value) {
@@ -197,7 +194,7 @@ k_code_tiles(const CodeArgs a) {
 #pragma unroll
           for (int u = 0; u < kKept; ++u) acc[t][n][u] *= up;
     }
-    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, part_sums);
+    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds);
   }
 }
 

@@ -211,7 +211,7 @@ int launch_int4_dequantize(const uint32_t* q, const float* scales, const uint8_t
 
 namespace {
 
-template <class E, int F, int RT, int NT, int GS>
+template <class E, int F, int RT, int NT, int GS, bool ZEROS>
 int launch_tiles(Int4Args a, hipStream_t stream) {
   constexpr int kRowsOfWave = RT * 16 / F;
   const int steps = ((a.tile.cols + 127) / 128 + F - 1) / F;
@@ -220,17 +220,24 @@ int launch_tiles(Int4Args a, hipStream_t stream) {
   a.tile.kw = kw;
   const int64_t rw = waves / kw, blocks = (units + rw - 1) / rw;
   const int64_t tokens = (a.tile.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
-  const size_t lds = (size_t)waves * RT * (16 / F) * NT * (16 / F) * sizeof(float);
-  hipLaunchKernelGGL((k_int4_tiles<E, F, RT, NT, GS>), dim3(grid_of(blocks), (unsigned)tokens), dim3(64 * waves), lds,
+  const size_t lds = (size_t)waves * NT * kXBytes;
+  hipLaunchKernelGGL((k_int4_tiles<E, F, RT, NT, GS, ZEROS>), dim3(grid_of(blocks), (unsigned)tokens), dim3(64 * waves), lds,
                      stream, a);
   return (int)hipGetLastError();
 }
 
+template <class E, int F, int RT, int NT, int GS>
+int launch_tiles_zeros(const Int4Args& a, hipStream_t stream) {
+  return a.zeros ? launch_tiles<E, F, RT, NT, GS, true>(a, stream) : launch_tiles<E, F, RT, NT, GS, false>(a, stream);
+}
+
+// One row tile in place of two or four for the shortest groups: their scales, asked for a step ahead,
+// fill the registers.
 template <class E, int F, int RT, int NT>
 int launch_tiles_group(const Int4Args& a, int64_t units, hipStream_t stream) {
-  return units % 4 == 0   ? launch_tiles<E, F, RT, NT, 4>(a, stream)
-         : units % 2 == 0 ? launch_tiles<E, F, RT, NT, 2>(a, stream)
-                          : launch_tiles<E, F, RT, NT, 1>(a, stream);
+  return units % 4 == 0   ? launch_tiles_zeros<E, F, RT, NT, 4>(a, stream)
+         : units % 2 == 0 ? launch_tiles_zeros<E, F, RT, NT, 2>(a, stream)
+                          : launch_tiles_zeros<E, F, (RT + 1) / 2, NT, 1>(a, stream);
 }
 
 // The largest fold that the tokens leave room for and the columns fill.
@@ -244,7 +251,7 @@ int launch_tiles_any(const Int4Args& a, int64_t per_group, hipStream_t stream) {
   if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_group<E, 4, 2, 1>(a, per_group, stream);
   if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_group<E, 2, 2, 1>(a, per_group, stream);
   if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_group<E, 1, 1, 1>(a, per_group, stream);
-  return launch_tiles_group<E, 1, 2, 2>(a, per_group, stream);
+  return launch_tiles_group<E, 1, 4, 2>(a, per_group, stream);
 }
 
 }  // namespace

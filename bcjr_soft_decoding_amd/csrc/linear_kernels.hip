@@ -51,20 +51,24 @@ int launch_tiles(CodeArgs a, hipStream_t stream) {
   constexpr int kRowsOfWave = RT * 16 / F;
   const int steps = (a.tile.cols / 128 + F - 1) / F;
   const int64_t units = (a.tile.rows + kRowsOfWave - 1) / kRowsOfWave;
-  const int kw = waves_along(steps, units);
+  // Every block makes a table: 8 waves share it, or as many as LDS leaves room for beside it (4 at 2^15
+  // states), and no more blocks than fit the chip are started.
+  auto lds_of = [&](int waves) { return ((size_t)1 << a.n) * sizeof(float) + (size_t)waves * NT * kXBytes; };
+  int waves = kMaxWaves;
+  while (lds_of(waves) > kLds) waves /= 2;
+  const size_t lds = lds_of(waves);
+  const int along = waves_along(steps, units), kw = along < waves ? along : waves;
   a.tile.kw = kw;
-  // every block makes a table: all 8 waves share it, and no more blocks than fit the chip are started
-  const int64_t rw = kMaxWaves / kw, blocks = (units + rw - 1) / rw;
+  const int64_t rw = waves / kw, blocks = (units + rw - 1) / rw;
   const int64_t tokens = (a.tile.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
-  const size_t lds = (((size_t)1 << a.n) + (size_t)kMaxWaves * RT * (16 / F) * NT * (16 / F)) * sizeof(float);
   const void* kernel = reinterpret_cast<const void*>(k_code_tiles<E, F, RT, NT, K>);
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return (int)e;
   }
-  const int64_t room = 256 * (lds > 81920 ? 1 : 2);
+  const int64_t room = 256 * (lds > kLds / 2 ? 1 : 2);
   hipLaunchKernelGGL((k_code_tiles<E, F, RT, NT, K>), dim3((unsigned)(blocks < room ? blocks : room), (unsigned)tokens),
-                     dim3(64 * kMaxWaves), lds, stream, a);
+                     dim3(64 * waves), lds, stream, a);
   return (int)hipGetLastError();
 }
 
@@ -86,7 +90,8 @@ int launch_tiles_any(const CodeArgs& a, int k, hipStream_t stream) {
   }
   if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_bits<E, 4, 2, 1>(a, k, stream);
   if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_bits<E, 2, 1, 1>(a, k, stream);
-  if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_bits<E, 1, 1, 1>(a, k, stream);
+  // beside 2^15 codewords there is no room for the x of two tiles of tokens
+  if (a.tile.tokens <= tile_tokens<E, 1>() || a.n == 15) return launch_tiles_bits<E, 1, 1, 1>(a, k, stream);
   return launch_tiles_bits<E, 1, 1, 2>(a, k, stream);
 }
 

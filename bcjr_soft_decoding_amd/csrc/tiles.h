@@ -1,12 +1,14 @@
 // Products of a few tokens with decoded weights on the matrix cores: the tile that the 4-bit and the
 // trellis-coded products share.
 //
-// A 16 x 16 x 32 matrix instruction multiplies 16 rows of weights with 16 columns of x. With few
-// tokens most of its columns would be idle, so the columns of W are folded F-fold: the tile's 16 rows are
-// 16 / F rows of W times F neighbouring blocks of 128 columns, its 16 columns are 16 / F tokens times
+// A 16 x 16 x 32 matrix instruction multiplies 16 rows of x with 16 rows of weights. With few tokens most of
+// its rows of x would be idle, so the columns of W are folded F-fold: the tile's 16 rows of weights are
+// 16 / F rows of W times F neighbouring blocks of 128 columns, its 16 rows of x are 16 / F tokens times
 // the same F blocks, and of the 16 x 16 sums those are kept whose blocks agree. One step of a
 // wave covers F blocks of a row in consecutive memory, and one row at F = 16: 2048 columns. fp32
-// inputs are three bfloat16 parts that add up to them exactly, each in a column of its own.
+// inputs are three bfloat16 parts that add up to them exactly, each in a row of its own. The weights
+// are the second operand: a lane's sums are then all of the row of W whose codes it read, and so is
+// the scale it needs.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -67,33 +69,14 @@ template <class T, int N> struct Loose;
 template <class T> struct Loose<T, 8> { typedef T V __attribute__((ext_vector_type(8), aligned(sizeof(T)))); };
 template <class T> struct Loose<T, 4> { typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T)))); };
 
-// x[col .. col + 7] as an operand, zeros from cols on.
-template <class E>
-__device__ inline typename TileOf<E>::T::V load_x8(const typename E::T* row, int col, int cols, int part) {
-  using V = typename TileOf<E>::T::V;
-  using X = typename E::T;
-  const X* p = row + col;
-  if constexpr (TileOf<E>::T::kParts == 1) {
-    if (col + 8 <= cols) return *reinterpret_cast<const typename Loose<X, 8>::V*>(p);
-    V v;
+// x[col .. col + 7], zeros from cols on.
+template <class X>
+__device__ inline typename Loose<X, 8>::V load_x8(const X* row, int col, int cols) {
+  if (col + 8 <= cols) return *reinterpret_cast<const typename Loose<X, 8>::V*>(row + col);
+  typename Loose<X, 8>::V v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? p[i] : (X)0.0f;
-    return v;
-  } else {
-    float f[8];
-    if (col + 8 <= cols) {
-      const auto a = *reinterpret_cast<const Loose<float, 4>::V*>(p), b = *reinterpret_cast<const Loose<float, 4>::V*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? p[i] : 0.0f;
-    }
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = part_of(f[2 * i], part) | part_of(f[2 * i + 1], part) << 16;
-    return __builtin_bit_cast(V, v);
-  }
+  for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? row[col + i] : (X)0.0f;
+  return v;
 }
 
 // floor(u / d) for u < 2^21 from the fp32 reciprocal of d: u + 1/2 is exact, and (u + 1/2) / d is at least 1 /
@@ -105,12 +88,12 @@ template <class E, int F>
 constexpr int tile_tokens() { return 16 / F / TileOf<E>::T::kParts; }
 constexpr int kMaxWaves = 8;
 
-// A lane's place: of the tile's rows and columns its operands are number c16, of the 32 products the
-// eight from 8 g on.
+// A lane's place: of the tile's rows of x and of weights its operands are number c16, of the 32 products
+// the eight from 8 g on.
 template <class E, int F>
 struct Place {
   static constexpr int kRows = 16 / F;                       // rows of W in a tile
-  static constexpr int kCols = 16 / F;                       // a tile's columns without their folds
+  static constexpr int kCols = 16 / F;                       // a tile's rows of x without their folds
   static constexpr int kKept = F == 1 ? 4 : F == 2 ? 2 : 1;  // sums of a lane that are kept
   static constexpr int kTokens = tile_tokens<E, F>();
   int c16, g, fold, col, wave, waves;
@@ -123,11 +106,11 @@ struct Place {
     fold = c16 % F;
     col = c16 / F;
   }
-  // Row of the tile that a lane's weights are of.
-  __device__ int weight_row() const { return c16 / F; }
-  // Row of the tile of kept sum u: the lane holds the sums of the tile's rows 4 g + i, and keeps those
-  // whose fold is its own.
-  __device__ int sum_row(int u) const {
+  // Row of W in the tile, of a lane's weights and of its sums.
+  __device__ int row() const { return c16 / F; }
+  // Row of x, without folds, of kept sum u: the lane holds the sums of the tile's rows 4 g + i of x, and keeps
+  // those whose fold is its own.
+  __device__ int sum_col(int u) const {
     const int i = F >= 4 ? c16 % 4 : F == 2 ? 2 * u + fold : u;
     return (4 * g + i) / F;
   }
@@ -138,22 +121,108 @@ struct Place {
     const float lo = c16 & 1 ? d[1] : d[0], hi = c16 & 1 ? d[3] : d[2];
     return c16 & 2 ? hi : lo;
   }
-  // x of column tile n, for tokens from m0 on: columns behind the last token repeat it.
-  __device__ const typename E::T* x_row(const TileArgs& a, long long m0, int n) const {
-    const long long m = m0 + n * kTokens + col / TileOf<E>::T::kParts;
-    return static_cast<const typename E::T*>(a.x) + (m < a.tokens ? m : a.tokens - 1) * a.xs;
+};
+
+// The x of one step of a wave, NT tiles of 16 rows of 128 columns. Neighbouring lanes load neighbouring
+// memory, 16 lanes a row: in the operands' own order every lane of a load would be in a row, and so a
+// cache line, of its own, and take a cycle of the cache instead of a quarter. The rows then go through LDS
+// (each wave its own kXBytes NT), where operands are read. Rows of no token are not loaded: what is left in
+// their place in LDS only reaches sums that are not kept.
+constexpr int kXStride = 256 + 16;        // bytes of a row: 8 lanes that read one chunk of 8 rows meet no bank twice
+constexpr int kXBytes = 16 * kXStride;
+
+template <class E, int F, int NT>
+struct XTile {
+  using T = typename TileOf<E>::T;
+  using V = typename T::V;
+  using X = typename E::T;
+  static constexpr int kParts = T::kParts, kTokens = tile_tokens<E, F>();
+  static constexpr int kLoads = (kTokens * F + 3) / 4;  // of four rows each
+  const X* row[NT][kLoads];
+  bool there[NT][kLoads];
+  typename Loose<X, 8>::V raw[NT][kLoads];
+
+  __device__ void init(const TileArgs& a, long long m0) {
+    const int r4 = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int token = (4 * i + r4) / F;
+        const long long m = m0 + n * kTokens + token;
+        there[n][i] = token < kTokens && m < a.tokens;
+        row[n][i] = static_cast<const X*>(a.x) + (there[n][i] ? m : 0) * a.xs;
+      }
   }
-  __device__ int x_part() const { return col % TileOf<E>::T::kParts; }
+  // Step s: blocks s F + fold.
+  __device__ void load(const TileArgs& a, int s) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int block = s * F + (4 * i + (lane >> 4)) % F;
+        if (there[n][i]) raw[n][i] = load_x8<X>(row[n][i], block * 128 + (lane & 15) * 8, a.cols);
+      }
+  }
+  __device__ void put(char* lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (!there[n][i]) continue;
+        const int r = 4 * i + (lane >> 4);
+        char* at = lds + n * kXBytes + (lane & 15) * 16;
+        if constexpr (kParts == 1) {
+          *reinterpret_cast<V*>(at + r * kXStride) = raw[n][i];
+        } else {
+          // three bfloat16 that add up to x: its leading 8 bits, the next 8 and the rest
+          u32x4 part[3];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            unsigned hi[2], mid[2], low[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x = raw[n][i][2 * j + k];
+              hi[k] = __float_as_uint(x);
+              const float left = x - __uint_as_float(hi[k] & 0xffff0000u);
+              mid[k] = __float_as_uint(left);
+              low[k] = __float_as_uint(left - __uint_as_float(mid[k] & 0xffff0000u));
+            }
+            part[0][j] = __builtin_amdgcn_perm(hi[1], hi[0], 0x07060302);
+            part[1][j] = __builtin_amdgcn_perm(mid[1], mid[0], 0x07060302);
+            part[2][j] = __builtin_amdgcn_perm(low[1], low[0], 0x07060302);
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<u32x4*>(at + ((r / F * 3 + p) * F + r % F) * kXStride) = part[p];
+        }
+      }
+    in_order();
+  }
+  // The operand of a lane from chunk `chunk` (8 columns) of its row.
+  static __device__ V get(const char* lds, const Place<E, F>& pl, int n, int chunk) {
+    return *reinterpret_cast<const V*>(lds + n * kXBytes + pl.c16 * kXStride + chunk * 16);
+  }
+  // Lanes of a wave read what others wrote: LDS works in order, the compiler has to as well.
+  static __device__ void in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
 };
 
 // The wave's sums over folds, the block's over waves and the parts of x, and the outputs. Rows
-// from row0 on belong to this wave's group of kw; part_sums [waves][RT][kRows][NT][kCols] in LDS.
+// from row0 on belong to this wave's group of kw. Sums [RT][kRows][NT][kCols] go to where each wave's x was.
 template <class E, int F, int RT, int NT>
 __device__ inline void join(const Place<E, F>& pl, const TileArgs& a, float (&acc)[RT][NT][Place<E, F>::kKept],
-                            long long first_unit, long long m0, float* part_sums) {
+                            long long first_unit, long long m0, char* lds) {
   using T = typename TileOf<E>::T;
   constexpr int kRows = Place<E, F>::kRows, kCols = Place<E, F>::kCols, kTokens = Place<E, F>::kTokens;
+  static_assert(RT * kRows * kCols * 4 <= kXBytes, "a wave's sums take the place of its x");
   const int c16 = pl.c16, g = pl.g, kw = a.kw, rw = pl.waves / kw;
+  float* mine_sums = reinterpret_cast<float*>(lds + pl.wave * NT * kXBytes);
+  XTile<E, F, NT>::in_order();
   // sums over the folds within the wave; for F > 4 only the lanes whose rows' folds are their own hold one
   const bool mine = F <= 4 || (F == 8 ? (c16 >> 2 & 1) == (g & 1) : c16 >> 2 == g);
 #pragma unroll
@@ -171,7 +240,7 @@ __device__ inline void join(const Place<E, F>& pl, const TileArgs& a, float (&ac
           v += __shfl_xor(v, 32, 64);
         }
         if (pl.fold == 0 && (F <= 4 || (F == 8 ? (g & 1) == 0 : g == 0)))
-          part_sums[(((pl.wave * RT + t) * kRows + pl.sum_row(u)) * NT + n) * kCols + pl.col] = v;
+          mine_sums[((t * kRows + pl.row()) * NT + n) * kCols + pl.sum_col(u)] = v;
       }
   __syncthreads();
   // one output at a time: over the waves of its rows and the parts of x
@@ -182,7 +251,8 @@ __device__ inline void join(const Place<E, F>& pl, const TileArgs& a, float (&ac
     if (r < a.rows && m < a.tokens) {
       float v = 0.0f;
       for (int k = 0; k < kw; ++k) {
-        const float* ps = part_sums + (((grp * kw + k) * RT * kRows + tr) * NT + mt / kTokens) * kCols + mt % kTokens * T::kParts;
+        const float* ps = reinterpret_cast<const float*>(lds + (grp * kw + k) * NT * kXBytes) +
+                          (tr * NT + mt / kTokens) * kCols + mt % kTokens * T::kParts;
 #pragma unroll
         for (int p = T::kParts - 1; p >= 0; --p) v += ps[p];
       }
@@ -193,6 +263,8 @@ __device__ inline void join(const Place<E, F>& pl, const TileArgs& a, float (&ac
 }
 
 }  // namespace
+
+constexpr size_t kLds = 160 * 1024;  // of a compute unit, all of which one block may take
 
 // Waves along a row while that leaves each at least one step and the chip is not yet full: 8
 // waves on each of 256 CUs.

@@ -98,36 +98,97 @@ __device__ inline int table_exponent(const float* codebook, int states, int* sha
   return max(e, -126);
 }
 
+// What a step of a wave reads.
+template <class E, int F, int RT, int NT, int K>
+struct CodeStep {
+  using T = typename TileOf<E>::T;
+  using V = typename T::V;
+  using X = XTile<E, F, NT>;
+  static constexpr int kKept = Place<E, F>::kKept;
+  static constexpr int kParts = std::is_same<E, F32>::value ? 3 : 2;
+  static constexpr int kShare = K <= 2 ? 8 : 4;  // states read from one 32-bit window: n + K (kShare - 1) <= 29
+  X x;
+  unsigned w[RT][K + 1];
+  float scale[RT];
+
+  // co, so: a lane's offsets in the rows' codes and scales. With TAIL some of the step's folds are not there.
+  template <bool TAIL>
+  __device__ void load(const CodeArgs& a, const Place<E, F>& pl, int s, const unsigned* __restrict__ code,
+                       const unsigned (&co)[RT], const float* __restrict__ scales, const unsigned (&so)[RT],
+                       const typename X::Rows& rows) {
+    const int block = s * F + pl.fold;
+    const bool in = !TAIL || block * 128 < a.tile.cols;
+    int chain = divide(block, a.reciprocal);
+    const unsigned at = chain * a.words + (block - chain * a.per_chain) * (4 * K);
+    if (TAIL) chain = min(chain, a.chains - 1);
+    const bool more = a.n > K;  // the last of the K + 1 words is there
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int i = 0; i <= K; ++i) w[t][i] = in && (i < K || more) ? code[co[t] + at + i] : 0u;
+      scale[t] = a.scales != nullptr ? scales[so[t] + chain] : 1.0f;
+    }
+    x.template load<TAIL>(a.tile, rows, s);
+  }
+
+  __device__ void add(const Place<E, F>& pl, char* lds, const char* table, int shift, unsigned mask,
+                      float (&acc)[RT][NT][kKept]) const {
+    x.put(lds);
+    V xo[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xo[n][j] = X::get(lds, pl, n, 4 * pl.g + j);
+    X::in_order();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      f32x4 d[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        unsigned e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
+          const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
+          e[i] = *reinterpret_cast<const unsigned*>(table + (window >> (shift - K * (i % kShare)) & mask));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) d[n] = add_products<T, kParts>(e, xo[n][j], d[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(scale[t], pl.kept(d[n], u), acc[t][n][u]);
+    }
+  }
+};
+
 // F folds, RT tiles of rows and NT tiles of tokens a wave, K bits a step.
 template <class E, int F, int RT, int NT, int K>
 __global__ void __launch_bounds__(64 * kMaxWaves)
 k_code_tiles(const CodeArgs a) {
-  using T = typename TileOf<E>::T;
-  using V = typename T::V;
   using Pl = Place<E, F>;
   constexpr int kRows = Pl::kRows, kKept = Pl::kKept;
-  constexpr int kParts = std::is_same<E, F32>::value ? 3 : 2;
-  constexpr int kShare = K <= 2 ? 8 : 4;  // states read from one 32-bit window: n + K (kShare - 1) <= 29
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int states = 1 << a.n;
   const Pl pl;
   char* mine = lds + pl.wave * NT * kXBytes;
-  unsigned* table = reinterpret_cast<unsigned*>(lds + pl.waves * NT * kXBytes);
+  char* table = lds + pl.waves * NT * kXBytes;
   const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(lds));
   const float down = ldexpf(1.0f, -top), up = ldexpf(1.0f, top);
-  for (int i = threadIdx.x; i < states; i += blockDim.x) table[i] = Codeword<E>::entry(a.codebook[i], down);
+  for (int i = threadIdx.x; i < states; i += blockDim.x)
+    reinterpret_cast<unsigned*>(table)[i] = Codeword<E>::entry(a.codebook[i], down);
   __syncthreads();
 
   const int kw = a.tile.kw, ki = pl.wave % kw, ri = pl.wave / kw, rw = pl.waves / kw;
-  const int blocks = a.tile.cols / 128, steps = (blocks + F - 1) / F;
+  const int whole = a.tile.cols / (F * 128), steps = whole + (whole * (F * 128) < a.tile.whole8() ? 1 : 0);
   const long long rows = a.tile.rows, units = (rows + RT * kRows - 1) / (RT * kRows);  // of rows, one for a wave
   const long long m0 = (long long)blockIdx.y * (NT * Pl::kTokens);
-  using X = XTile<E, F, NT>;
-  X x;
-  x.init(a.tile, m0);
+  const XRows<E, F, NT> xrows(a.tile, m0);
   const unsigned mask = (unsigned)(states - 1) << 2;
   const int shift = 30 - a.n;  // a state at the top of a window as the byte offset of its codeword
-  const int more = a.n > K;    // the last of the K + 1 words is there
 
   for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
     const long long row0 = (ub + ri) * (RT * kRows);
@@ -143,48 +204,19 @@ k_code_tiles(const CodeArgs a) {
       so[t] = (unsigned)(min(t * kRows + pl.row(), last) * a.chains);
       co[t] = so[t] * a.words + K * pl.g;
     }
-    for (int s = ki; s < steps; s += kw) {
-      const int block = s * F + pl.fold;
-      const bool in = block < blocks;
-      const int chain = min(divide(block, a.reciprocal), a.chains - 1);
-      const unsigned at = chain * a.words + (block - chain * a.per_chain) * (4 * K);
-      unsigned w[RT][K + 1];
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i <= K; ++i) w[t][i] = in && (i < K || more) ? code[co[t] + at + i] : 0u;
-      x.load(a.tile, s);
-      x.put(mine);
-      V xo[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xo[n][j] = X::get(mine, pl, n, 4 * pl.g + j);
-      X::in_order();
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        f32x4 d[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          unsigned e[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
-            const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
-            const unsigned byte = window >> (shift - K * (i % kShare)) & mask;
-            e[i] = *reinterpret_cast<const unsigned*>(reinterpret_cast<const char*>(table) + byte);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) d[n] = add_products<T, kParts>(e, xo[n][j], d[n]);
-        }
-        const float sc = a.scales != nullptr ? scales[so[t] + chain] : 1.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(sc, pl.kept(d[n], u), acc[t][n][u]);
-      }
+    CodeStep<E, F, RT, NT, K> one, two;
+    auto load = [&](auto& step, int s) {
+      if (s < whole)
+        step.template load<false>(a, pl, s, code, co, scales, so, xrows);
+      else
+        step.template load<true>(a, pl, s, code, co, scales, so, xrows);
+    };
+    if (ki < steps) load(one, ki);
+    for (int s = ki; s < steps; s += 2 * kw) {
+      if (s + kw < steps) load(two, s + kw);
+      one.add(pl, mine, table, shift, mask, acc);
+      if (s + 2 * kw < steps) load(one, s + 2 * kw);
+      if (s + kw < steps) two.add(pl, mine, table, shift, mask, acc);
     }
     if constexpr (std::is_same<E, F16>::value) {
 #pragma unroll
@@ -194,7 +226,7 @@ k_code_tiles(const CodeArgs a) {
 #pragma unroll
           for (int u = 0; u < kKept; ++u) acc[t][n][u] *= up;
     }
-    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds);
+    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds, [](long long, const typename E::T*) { return 0.0f; });
   }
 }
 

@@ -11,13 +11,6 @@
 namespace bcjr {
 namespace {
 
-// The word of a row that holds columns 8 u .. 8 u + 7.
-__device__ inline long long word_of(long long u) {
-  return (u & ~15ll) + 4 * (u & 3) + ((u >> 2) & 3);
-}
-// The low bit of column c (0 .. 7) of a word.
-__device__ inline int nibble_shift(int c) { return 4 * ((c >> 1) + 4 * (c & 1)); }
-
 // rint(w / s) for s > 0 as exact division gives it, by = 1 / s to an ulp: the product is at most one off,
 // and the sign of w - (q +- 1/2) s, which a fused multiply-add keeps, says so; a tie goes to the even code.
 __device__ inline float rint_quotient(float w, float s, float by) {
@@ -231,13 +224,19 @@ int launch_tiles_zeros(const Int4Args& a, hipStream_t stream) {
   return a.zeros ? launch_tiles<E, F, RT, NT, GS, true>(a, stream) : launch_tiles<E, F, RT, NT, GS, false>(a, stream);
 }
 
-// One row tile in place of two or four for the shortest groups: their scales, asked for a step ahead,
-// fill the registers.
 template <class E, int F, int RT, int NT>
 int launch_tiles_group(const Int4Args& a, int64_t units, hipStream_t stream) {
   return units % 4 == 0   ? launch_tiles_zeros<E, F, RT, NT, 4>(a, stream)
          : units % 2 == 0 ? launch_tiles_zeros<E, F, RT, NT, 2>(a, stream)
-                          : launch_tiles_zeros<E, F, (RT + 1) / 2, NT, 1>(a, stream);
+                          : launch_tiles_zeros<E, F, RT, NT, 1>(a, stream);
+}
+
+// Four row tiles a wave, which share the loads of x, where that leaves waves enough.
+template <class E, int F>
+int launch_tiles_rows(const Int4Args& a, int64_t per_group, hipStream_t stream) {
+  const int64_t steps = ((a.tile.cols + 127) / 128 + F - 1) / F, along = steps < kMaxWaves ? steps : kMaxWaves;
+  const bool four = a.tile.rows * F / 64 * along >= 1024;
+  return four ? launch_tiles_group<E, F, 4, 1>(a, per_group, stream) : launch_tiles_group<E, F, 1, 1>(a, per_group, stream);
 }
 
 // The largest fold that the tokens leave room for and the columns fill.
@@ -245,12 +244,12 @@ template <class E>
 int launch_tiles_any(const Int4Args& a, int64_t per_group, hipStream_t stream) {
   const int blocks = (a.tile.cols + 127) / 128;
   if constexpr (TileOf<E>::T::kParts == 1) {
-    if (a.tile.tokens == 1 && blocks > 8) return launch_tiles_group<E, 16, 4, 1>(a, per_group, stream);
-    if (a.tile.tokens <= 2 && blocks > 4) return launch_tiles_group<E, 8, 4, 1>(a, per_group, stream);
+    if (a.tile.tokens == 1 && blocks > 8) return launch_tiles_rows<E, 16>(a, per_group, stream);
+    if (a.tile.tokens <= 2 && blocks > 4) return launch_tiles_rows<E, 8>(a, per_group, stream);
   }
-  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_group<E, 4, 2, 1>(a, per_group, stream);
-  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_group<E, 2, 2, 1>(a, per_group, stream);
-  if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_group<E, 1, 1, 1>(a, per_group, stream);
+  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_rows<E, 4>(a, per_group, stream);
+  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_rows<E, 2>(a, per_group, stream);
+  if (a.tile.tokens <= tile_tokens<E, 1>()) return launch_tiles_rows<E, 1>(a, per_group, stream);
   return launch_tiles_group<E, 1, 4, 2>(a, per_group, stream);
 }
 

@@ -20,14 +20,23 @@ struct Int4Args {
 
 namespace {
 
+// The word of a row that holds columns 8 u .. 8 u + 7.
+__device__ inline long long word_of(long long u) {
+  return (u & ~15ll) + 4 * (u & 3) + ((u >> 2) & 3);
+}
+// The low bit of column c (0 .. 7) of a word.
+__device__ inline int nibble_shift(int c) { return 4 * ((c >> 1) + 4 * (c & 1)); }
+
 // The eight weights of a word as numbers 1 + q / 16.
 template <class T>
-__device__ inline typename T::V weights8(unsigned w) {
+__device__ inline typename T::V weights8(unsigned w, unsigned one) {
   u32x4 v;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int up = T::kUp - 4 * p;
-    v[p] = ((up >= 0 ? w << up : w >> -up) & T::kMask) | T::kOne;
+    const unsigned at = up >= 0 ? w << up : w >> -up;
+    // one instruction, which the compiler makes of two constants only if one of them is in a vector register
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(v[p]) : "v"(at), "s"(T::kMask), "v"(one));
   }
   return __builtin_bit_cast(typename T::V, v);
 }
@@ -63,23 +72,26 @@ struct Int4Step {
   float scale[kGroups];
   unsigned zero[kGroups];
 
-  // qo: a lane's offset in the codes of tile t's step 0; so: its row of tile g in the scales.
-  __device__ void load(const Int4Args& a, const Place<E, F>& pl, int s, int blocks, const unsigned* __restrict__ q,
+  // q: the codes of step s, qo: a lane's offset there in tile t; so: its row of tile g in the scales. With TAIL
+  // some of the step's columns, and some folds, are not there.
+  template <bool TAIL>
+  __device__ void load(const Int4Args& a, const Place<E, F>& pl, int s, const unsigned* __restrict__ q,
                        const unsigned (&qo)[RT], const float* __restrict__ scales, const uint8_t* __restrict__ zeros,
-                       unsigned so) {
+                       unsigned so, const typename X::Rows& rows) {
     const int lane = threadIdx.x & 63;
-    const bool in = s * F + (lane >> 2) % F < blocks;  // folds behind the last block have no codes
+    const bool in = !TAIL || (s * F + (lane >> 2) % F) * 128 < a.tile.cols;  // codes end with the last block
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      w[t] = in ? *reinterpret_cast<const u32x4*>(q + (qo[t] + s * (F * 16))) : u32x4{0, 0, 0, 0};
+      w[t] = in ? *reinterpret_cast<const u32x4*>(q + s * (F * 16) + qo[t]) : u32x4{0, 0, 0, 0};
     const int unit = (s * F + pl.fold) * 4;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      const int group = min(divide(unit + i * GS, a.per_group), a.groups - 1);
+      int group = divide(unit + i * GS, a.per_group);
+      if (TAIL) group = min(group, a.groups - 1);
       scale[i] = scales[so + group];
       if (ZEROS) zero[i] = zeros[so + group];
     }
-    x.load(a.tile, s);
+    x.template load<TAIL>(a.tile, rows, s);
   }
 
   __device__ void add(const Place<E, F>& pl, char* lds, float (&acc)[RT][NT][kKept]) {
@@ -95,7 +107,9 @@ struct Int4Step {
 #pragma unroll
       for (int j = 0; j < 4; ++j) xo[n][j] = X::get(lds, pl, n, 4 * j + pl.g);
     X::in_order();
-    const V ones = __builtin_bit_cast(V, u32x4{T::kOne, T::kOne, T::kOne, T::kOne});
+    unsigned one = T::kOne;
+    asm("" : "+v"(one));  // kept in a vector register
+    const V ones = __builtin_bit_cast(V, u32x4{one, one, one, one});
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       f32x4 sum[NT];
@@ -115,7 +129,7 @@ struct Int4Step {
         for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = i * GS; j < i * GS + GS; ++j) {
-          const V wj = weights8<T>(w[t][j]);
+          const V wj = weights8<T>(w[t][j], one);
 #pragma unroll
           for (int n = 0; n < NT; ++n) d[n] = T::mfma(xo[n][j], wj, d[n]);
         }
@@ -140,10 +154,11 @@ k_int4_tiles(const Int4Args a) {
   const Pl pl;
   char* mine = lds + pl.wave * NT * kXBytes;
   const int kw = a.tile.kw, ki = pl.wave % kw, ri = pl.wave / kw, rw = pl.waves / kw;
-  const int blocks = (a.tile.cols + 127) / 128, steps = (blocks + F - 1) / F;
+  const int whole = a.tile.cols / (F * 128), steps = whole + (whole * (F * 128) < a.tile.whole8() ? 1 : 0);
   const long long rows = a.tile.rows, units = (rows + RT * kRows - 1) / (RT * kRows);  // of rows, one for a wave
   const long long m0 = (long long)blockIdx.y * (NT * Pl::kTokens);
   const int lane = threadIdx.x & 63;
+  const XRows<E, F, NT> xrows(a.tile, m0);
 
   for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
     const long long row0 = (ub + ri) * (RT * kRows);
@@ -160,13 +175,17 @@ k_int4_tiles(const Int4Args a) {
       qo[t] = (unsigned)(min(t * kRows + (lane >> 2) / F, last) * a.words + (lane >> 2) % F * 16 + 4 * (lane & 3));
     const unsigned so = (unsigned)(min(min(pl.g, RT - 1) * kRows + pl.row(), last) * a.groups);
     Int4Step<E, F, RT, NT, GS, ZEROS> one, two;
-    one.x.init(a.tile, m0);
-    two.x.init(a.tile, m0);
-    if (ki < steps) one.load(a, pl, ki, blocks, q, qo, scales, zeros, so);
+    auto load = [&](auto& step, int s) {
+      if (s < whole)
+        step.template load<false>(a, pl, s, q, qo, scales, zeros, so, xrows);
+      else
+        step.template load<true>(a, pl, s, q, qo, scales, zeros, so, xrows);
+    };
+    if (ki < steps) load(one, ki);
     for (int s = ki; s < steps; s += 2 * kw) {
-      if (s + kw < steps) two.load(a, pl, s + kw, blocks, q, qo, scales, zeros, so);
+      if (s + kw < steps) load(two, s + kw);
       one.add(pl, mine, acc);
-      if (s + 2 * kw < steps) one.load(a, pl, s + 2 * kw, blocks, q, qo, scales, zeros, so);
+      if (s + 2 * kw < steps) load(one, s + 2 * kw);
       if (s + kw < steps) two.add(pl, mine, acc);
     }
     // codes were sixteenths
@@ -176,7 +195,17 @@ k_int4_tiles(const Int4Args a) {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < kKept; ++u) acc[t][n][u] *= 16.0f;
-    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds);
+    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds, [&](long long r, const typename E::T* x) {
+      const int c8 = a.tile.whole8();
+      float sum = 0.0f;
+      if (c8 < a.tile.cols) {  // all in one word and one group
+        const unsigned word = a.q[r * a.words + word_of(c8 / 8)];
+        const float z = ZEROS ? (float)a.zeros[r * a.groups + a.groups - 1] : 8.0f;
+        for (int c = c8; c < a.tile.cols; ++c) sum = fmaf((float)(word >> nibble_shift(c - c8) & 15u) - z, E::load(x + c), sum);
+        sum *= a.scales[r * a.groups + a.groups - 1];
+      }
+      return sum;
+    });
   }
 }
 

@@ -26,6 +26,8 @@ struct TileArgs {
   long long rows, tokens, xs, ys;
   int cols;
   int kw;  // waves of a block that share a row, each with every kw-th step
+  // Columns that whole loads of eight cover. The up to seven others, if any, are added to the outputs (join()).
+  __host__ __device__ int whole8() const { return cols & ~7; }
 };
 
 namespace {
@@ -68,16 +70,6 @@ __device__ inline unsigned part_of(float x, int part) {
 template <class T, int N> struct Loose;
 template <class T> struct Loose<T, 8> { typedef T V __attribute__((ext_vector_type(8), aligned(sizeof(T)))); };
 template <class T> struct Loose<T, 4> { typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T)))); };
-
-// x[col .. col + 7], zeros from cols on.
-template <class X>
-__device__ inline typename Loose<X, 8>::V load_x8(const X* row, int col, int cols) {
-  if (col + 8 <= cols) return *reinterpret_cast<const typename Loose<X, 8>::V*>(row + col);
-  typename Loose<X, 8>::V v;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? row[col + i] : (X)0.0f;
-  return v;
-}
 
 // floor(u / d) for u < 2^21 from the fp32 reciprocal of d: u + 1/2 is exact, and (u + 1/2) / d is at least 1 /
 // (2 d) off any whole number, more than the two roundings' u / d 2^-23.
@@ -126,43 +118,54 @@ struct Place {
 // The x of one step of a wave, NT tiles of 16 rows of 128 columns. Neighbouring lanes load neighbouring
 // memory, 16 lanes a row: in the operands' own order every lane of a load would be in a row, and so a
 // cache line, of its own, and take a cycle of the cache instead of a quarter. The rows then go through LDS
-// (each wave its own kXBytes NT), where operands are read. Rows of no token are not loaded: what is left in
-// their place in LDS only reaches sums that are not kept.
+// (each wave its own kXBytes NT), where operands are read.
 constexpr int kXStride = 256 + 16;        // bytes of a row: 8 lanes that read one chunk of 8 rows meet no bank twice
 constexpr int kXBytes = 16 * kXStride;
+
+// Where a lane's loads begin, from the first token's row on (in_pieces() sees to it that 32 bits hold that):
+// rows behind the last token repeat it (their sums are not kept).
+template <class E, int F, int NT>
+struct XRows {
+  static constexpr int kTokens = tile_tokens<E, F>();
+  static constexpr int kLoads = (kTokens * F + 3) / 4;  // of four rows each
+  const typename E::T* first;
+  unsigned at[NT][kLoads];
+  __device__ XRows(const TileArgs& a, long long m0) {
+    const int lane = threadIdx.x & 63;
+    const int last = (int)(a.tokens - 1 - m0 < NT * kTokens ? a.tokens - 1 - m0 : NT * kTokens);
+    first = static_cast<const typename E::T*>(a.x) + m0 * a.xs;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        at[n][i] = (unsigned)min(n * kTokens + r / F, last) * (unsigned)a.xs + r % F * 128 + (lane & 15) * 8;
+      }
+  }
+};
 
 template <class E, int F, int NT>
 struct XTile {
   using T = typename TileOf<E>::T;
   using V = typename T::V;
   using X = typename E::T;
-  static constexpr int kParts = T::kParts, kTokens = tile_tokens<E, F>();
-  static constexpr int kLoads = (kTokens * F + 3) / 4;  // of four rows each
-  const X* row[NT][kLoads];
-  bool there[NT][kLoads];
+  using Rows = XRows<E, F, NT>;
+  static constexpr int kParts = T::kParts, kTokens = tile_tokens<E, F>(), kLoads = Rows::kLoads;
   typename Loose<X, 8>::V raw[NT][kLoads];
 
-  __device__ void init(const TileArgs& a, long long m0) {
-    const int r4 = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int token = (4 * i + r4) / F;
-        const long long m = m0 + n * kTokens + token;
-        there[n][i] = token < kTokens && m < a.tokens;
-        row[n][i] = static_cast<const X*>(a.x) + (there[n][i] ? m : 0) * a.xs;
-      }
-  }
-  // Step s: blocks s F + fold.
-  __device__ void load(const TileArgs& a, int s) {
+  // Step s: columns s F 128 and on. With TAIL those from a.whole8() on are not there and are zero.
+  template <bool TAIL>
+  __device__ void load(const TileArgs& a, const Rows& rows, int s) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int block = s * F + (4 * i + (lane >> 4)) % F;
-        if (there[n][i]) raw[n][i] = load_x8<X>(row[n][i], block * 128 + (lane & 15) * 8, a.cols);
+        const auto* p = reinterpret_cast<const typename Loose<X, 8>::V*>(rows.first + s * (F * 128) + rows.at[n][i]);
+        if (!TAIL || s * (F * 128) + (4 * i + (lane >> 4)) % F * 128 + (lane & 15) * 8 < a.whole8())
+          raw[n][i] = *p;
+        else
+          raw[n][i] = typename Loose<X, 8>::V{};
       }
   }
   __device__ void put(char* lds) const {
@@ -171,7 +174,6 @@ struct XTile {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        if (!there[n][i]) continue;
         const int r = 4 * i + (lane >> 4);
         char* at = lds + n * kXBytes + (lane & 15) * 16;
         if constexpr (kParts == 1) {
@@ -194,9 +196,10 @@ struct XTile {
             part[1][j] = __builtin_amdgcn_perm(mid[1], mid[0], 0x07060302);
             part[2][j] = __builtin_amdgcn_perm(low[1], low[0], 0x07060302);
           }
+          if (kLoads * 4 == kTokens * F || r < kTokens * F)
 #pragma unroll
-          for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<u32x4*>(at + ((r / F * 3 + p) * F + r % F) * kXStride) = part[p];
+            for (int p = 0; p < 3; ++p)
+              *reinterpret_cast<u32x4*>(at + ((r / F * 3 + p) * F + r % F) * kXStride) = part[p];
         }
       }
     in_order();
@@ -212,50 +215,45 @@ struct XTile {
   }
 };
 
-// The wave's sums over folds, the block's over waves and the parts of x, and the outputs. Rows
-// from row0 on belong to this wave's group of kw. Sums [RT][kRows][NT][kCols] go to where each wave's x was.
-template <class E, int F, int RT, int NT>
+// The outputs: sums over the block's waves that share rows, the parts of x and the folds, and rest(row, x) for the
+// columns behind the last eight. The kept sums [RT][kRows][NT][kCols][F] go to where each wave's x was.
+template <class E, int F, int RT, int NT, class Rest>
 __device__ inline void join(const Place<E, F>& pl, const TileArgs& a, float (&acc)[RT][NT][Place<E, F>::kKept],
-                            long long first_unit, long long m0, char* lds) {
-  using T = typename TileOf<E>::T;
-  constexpr int kRows = Place<E, F>::kRows, kCols = Place<E, F>::kCols, kTokens = Place<E, F>::kTokens;
-  static_assert(RT * kRows * kCols * 4 <= kXBytes, "a wave's sums take the place of its x");
-  const int c16 = pl.c16, g = pl.g, kw = a.kw, rw = pl.waves / kw;
-  float* mine_sums = reinterpret_cast<float*>(lds + pl.wave * NT * kXBytes);
+                            long long first_unit, long long m0, char* lds, Rest rest) {
+  using P = Place<E, F>;
+  constexpr int kParts = TileOf<E>::T::kParts, kRows = P::kRows, kCols = P::kCols, kTokens = P::kTokens;
+  static_assert(RT * kRows * kCols * F * 4 <= kXBytes, "a wave's sums take the place of its x");
+  const int kw = a.kw, rw = pl.waves / kw;
+  float* sums = reinterpret_cast<float*>(lds + pl.wave * NT * kXBytes);
   XTile<E, F, NT>::in_order();
-  // sums over the folds within the wave; for F > 4 only the lanes whose rows' folds are their own hold one
-  const bool mine = F <= 4 || (F == 8 ? (c16 >> 2 & 1) == (g & 1) : c16 >> 2 == g);
+  // for F > 4 only the lanes whose rows of x have their own fold hold a sum
+  const bool mine = F <= 4 || (F == 8 ? (pl.c16 >> 2 & 1) == (pl.g & 1) : pl.c16 >> 2 == pl.g);
+  if (mine) {
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int u = 0; u < Place<E, F>::kKept; ++u) {
-        float v = mine ? acc[t][n][u] : 0.0f;
-#pragma unroll
-        for (int d = 1; d < F; d <<= 1) v += __shfl_xor(v, d, 64);
-        if constexpr (F == 8) v += __shfl_xor(v, 16, 64);
-        if constexpr (F == 16) {
-          v += __shfl_xor(v, 16, 64);
-          v += __shfl_xor(v, 32, 64);
-        }
-        if (pl.fold == 0 && (F <= 4 || (F == 8 ? (g & 1) == 0 : g == 0)))
-          mine_sums[((t * kRows + pl.row()) * NT + n) * kCols + pl.sum_col(u)] = v;
-      }
+        for (int u = 0; u < P::kKept; ++u)
+          sums[(((t * kRows + pl.row()) * NT + n) * kCols + pl.sum_col(u)) * F + pl.fold] = acc[t][n][u];
+  }
   __syncthreads();
-  // one output at a time: over the waves of its rows and the parts of x
-  const int outs = RT * kRows * NT * kTokens;
-  for (int o = threadIdx.x; o < rw * outs; o += blockDim.x) {
-    const int grp = o / outs, rest = o - grp * outs, tr = rest / (NT * kTokens), mt = rest % (NT * kTokens);
-    const long long r = (first_unit + grp) * (RT * kRows) + tr, m = m0 + mt;
-    if (r < a.rows && m < a.tokens) {
-      float v = 0.0f;
-      for (int k = 0; k < kw; ++k) {
-        const float* ps = reinterpret_cast<const float*>(lds + (grp * kw + k) * NT * kXBytes) +
-                          (tr * NT + mt / kTokens) * kCols + mt % kTokens * T::kParts;
+  // F neighbouring lanes an output, each a fold
+  constexpr int kOuts = RT * kRows * NT * kTokens;
+  for (int o = threadIdx.x / F; o < rw * kOuts; o += blockDim.x / F) {
+    const int grp = o / kOuts, out = o % kOuts, tr = out / (NT * kTokens), mt = out % (NT * kTokens);
+    const int at = ((tr * NT + mt / kTokens) * kCols + mt % kTokens * kParts) * F + threadIdx.x % F;
+    float v = 0.0f;
+    for (int k = 0; k < kw; ++k) {
+      const float* s = reinterpret_cast<const float*>(lds + (grp * kw + k) * NT * kXBytes) + at;
 #pragma unroll
-        for (int p = T::kParts - 1; p >= 0; --p) v += ps[p];
-      }
+      for (int p = kParts - 1; p >= 0; --p) v += s[p * F];
+    }
+#pragma unroll
+    for (int d = 1; d < F; d <<= 1) v += __shfl_xor(v, d, 64);
+    const long long r = (first_unit + grp) * (RT * kRows) + tr, m = m0 + mt;
+    if (threadIdx.x % F == 0 && r < a.rows && m < a.tokens) {
+      v += rest(r, static_cast<const typename E::T*>(a.x) + m * a.xs);
       E::store(static_cast<typename E::T*>(a.y) + m * a.ys + r, v);
     }
   }
@@ -290,10 +288,11 @@ inline TileArgs tile_args(const MatvecIO& io, int64_t rows, int64_t cols) {
   return t;
 }
 
-// Calls f with the tokens in pieces that one launch's grid holds: 32768 tiles of at least 5.
+// Calls f with the tokens in pieces that one launch's grid holds, 32768 tiles of at least 5, or, where the rows of
+// x lie so far apart that 32-bit offsets do not reach over 32 of them, one by one.
 template <class Fn>
 inline int in_pieces(MatvecIO io, int dtype_size, Fn f) {
-  const int64_t most = 5 * 32768, total = io.tokens;
+  const int64_t most = io.x_stride < ((int64_t)1 << 24) + 1 ? 5 * 32768 : 1, total = io.tokens;
   for (int64_t m = 0; m < total; m += most) {
     MatvecIO p = io;
     p.tokens = total - m < most ? total - m : most;

@@ -36,6 +36,9 @@ SOURCES = ["host.cpp", "sparse_kernels.hip", "viterbi_kernels.hip", "dense_kerne
 # scheduler that maximises instruction-level parallelism (see ilp_fwd_shape / ilp_bwd_shape).
 ILP_FLAGS = ["-DBCJR_ILP_TU", "-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 EXTRA_UNITS = [("sparse_kernels.hip", "sparse_kernels_ilp", ILP_FLAGS)]
+# code_tiles.hip is built once for each type of x.
+EXTRA_UNITS += [("code_tiles.hip", f"code_tiles_{t}", [f"-DCODE_TYPE={t.upper()}", f"-DCODE_NAME={t}"])
+                for t in ("f32", "f16", "bf16")]
 # The forward-backward kernels' max reductions need no NaN canonicalisation: a NaN or Inf input
 # still reaches the outputs through the exponentials and sums that follow every max (the
 # propagation the C ABI documents is tested); the Viterbi decoder keeps strict IEEE semantics

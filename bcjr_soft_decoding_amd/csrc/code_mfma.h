@@ -3,79 +3,61 @@
 // A lane decodes 32 neighbouring weights of a chain: they begin at a whole word of its code, whatever
 // k, and lie in k + 1 words. A window of the bit string is two words shifted into one, which holds the
 // states of several neighbours; a state is a shift and a mask away, and its codeword one read of a
-// table in LDS. The table holds a codeword as two 16-bit parts, c = hi + lo to 2^-16 (bfloat16) or
-// 2^-21 (half) of c, each multiplied on its own: one read serves both, and rounding weights to 16 bits
-// alone would cost as much precision as rounding the result. fp32 inputs get fp32 codewords, taken
-// apart into three bfloat16 after the read.
+// table in LDS. For 16-bit x the table holds a codeword as two parts, c = hi + lo to 2^-16 (bfloat16)
+// or 2^-21 (half) of c, in the halves of a word (rounding weights to 16 bits alone would cost as much precision
+// as rounding the result), and that word goes into the matrix operand as it is: the two parts are
+// neighbours in the sum's index, and x is there twice. For fp32 x it holds three bfloat16 parts and a
+// zero. Where it is small enough the table goes by windows of two states and gives two neighbours
+// in one read: LDS serves 6.7 random 8-byte reads a clock and 8.8 of 4 bytes.
 #pragma once
 #include "tiles.h"
 
 namespace bcjr {
 
-struct CodeArgs {
-  TileArgs tile;
-  const unsigned* code;
-  const float* codebook;
-  const float* scales;         // of a chain, or NULL
-  int n, chains, words;        // state bits; chains of a row; words of a chain
-  int per_chain;               // blocks of 128 columns in a chain
-  float reciprocal;            // 1 / per_chain
-};
-
 namespace {
 
-// Part sums of 8 weights: what the table holds for a type, and its products with x.
+// What the table holds of a codeword: words of two neighbouring terms of the sum.
 template <class E>
-struct Codeword {  // bfloat16: hi in the upper half, lo in the lower
-  static __device__ unsigned entry(float c, float) {
+struct Codeword {  // bfloat16
+  static constexpr int kWords = 1;
+  static __device__ void write(unsigned* at, float c, float) {
     const __bf16 hi = (__bf16)c, lo = (__bf16)(c - (float)hi);
-    return (unsigned)__builtin_bit_cast(unsigned short, hi) << 16 | __builtin_bit_cast(unsigned short, lo);
+    at[0] = (unsigned)__builtin_bit_cast(unsigned short, lo) << 16 | __builtin_bit_cast(unsigned short, hi);
   }
 };
 template <>
 struct Codeword<F16> {  // half, the codebook scaled by a power of two that brings its largest to [2^13, 2^14)
-  static __device__ unsigned entry(float c, float scale) {
+  static constexpr int kWords = 1;
+  static __device__ void write(unsigned* at, float c, float scale) {
     c *= scale;
     const _Float16 hi = (_Float16)c, lo = (_Float16)(c - (float)hi);
-    return (unsigned)__builtin_bit_cast(unsigned short, hi) << 16 | __builtin_bit_cast(unsigned short, lo);
+    at[0] = (unsigned)__builtin_bit_cast(unsigned short, lo) << 16 | __builtin_bit_cast(unsigned short, hi);
   }
 };
 template <>
-struct Codeword<F32> {
-  static __device__ unsigned entry(float c, float) { return __float_as_uint(c); }
+struct Codeword<F32> {  // the leading 8 bits, the next 8, the rest
+  static constexpr int kWords = 2;
+  static __device__ void write(unsigned* at, float c, float) {
+    const unsigned hi = __float_as_uint(c);
+    const float left = c - __uint_as_float(hi & 0xffff0000u);
+    const unsigned mid = __float_as_uint(left);
+    at[0] = __builtin_amdgcn_perm(mid, hi, 0x07060302);
+    at[1] = __float_as_uint(left - __uint_as_float(mid & 0xffff0000u)) >> 16;
+  }
 };
 
-template <class T, int PARTS>
-__device__ inline f32x4 add_products(const unsigned (&e)[8], typename T::V x, f32x4 d) {
-  if constexpr (PARTS == 2) {
-    u32x4 hi, lo;
+// f(i, c(i)) for the block's share of the codewords, loaded four at a time, several loads in flight.
+template <class Fn>
+__device__ inline void each_codeword(const float* codebook, int states, Fn f) {
+  if (states < 4) {
+    if ((int)threadIdx.x < states) f(threadIdx.x, codebook[threadIdx.x]);
+    return;
+  }
+#pragma unroll 4
+  for (int i = 4 * threadIdx.x; i < states; i += 4 * blockDim.x) {
+    const auto v = *reinterpret_cast<const Loose<float, 4>::V*>(codebook + i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hi[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x07060302);
-      lo[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x05040100);
-    }
-    d = T::mfma(x, __builtin_bit_cast(typename T::V, lo), d);
-    return T::mfma(x, __builtin_bit_cast(typename T::V, hi), d);
-  } else {
-    u32x4 p[3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float r[2];
-      unsigned mid[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const unsigned u = e[2 * i + j];
-        r[j] = __uint_as_float(u) - __uint_as_float(u & 0xffff0000u);
-        mid[j] = __float_as_uint(r[j]);
-        r[j] -= __uint_as_float(mid[j] & 0xffff0000u);
-      }
-      p[0][i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x07060302);
-      p[1][i] = __builtin_amdgcn_perm(mid[1], mid[0], 0x07060302);
-      p[2][i] = __builtin_amdgcn_perm(__float_as_uint(r[1]), __float_as_uint(r[0]), 0x07060302);
-    }
-#pragma unroll
-    for (int i = 2; i >= 0; --i) d = T::mfma(x, __builtin_bit_cast(typename T::V, p[i]), d);
-    return d;
+    for (int j = 0; j < 4; ++j) f(i + j, v[j]);
   }
 }
 
@@ -87,10 +69,10 @@ __device__ inline int table_exponent(const float* codebook, int states, int* sha
   if (threadIdx.x == 0) *shared = 0;
   __syncthreads();
   int top = 0;
-  for (int i = threadIdx.x; i < states; i += blockDim.x) {
-    const int e = __float_as_uint(codebook[i]) >> 23 & 0xff;
+  each_codeword(codebook, states, [&](int, float c) {
+    const int e = __float_as_uint(c) >> 23 & 0xff;
     if (e < 255) top = max(top, e);
-  }
+  });
   for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d, 64));
   if ((threadIdx.x & 63) == 0) atomicMax(shared, top);
   __syncthreads();
@@ -98,75 +80,153 @@ __device__ inline int table_exponent(const float* codebook, int states, int* sha
   return max(e, -126);
 }
 
+// The table in LDS, at offset 0: [2^n] codewords, or with PAIR [2^(n + K)] of two neighbours' windows.
+template <class E, int K, bool PAIR>
+struct Table {
+  static constexpr int kWords = Codeword<E>::kWords * (PAIR ? 2 : 1);  // of an entry
+  static constexpr int kBytes = 4 * kWords, kShift = kWords == 1 ? 2 : kWords == 2 ? 3 : 4;
+  typedef unsigned Entry __attribute__((ext_vector_type(kWords)));
+  static __host__ __device__ size_t bytes(int n) { return ((size_t)kBytes << n) << (PAIR ? K : 0); }
+
+  static __device__ void make(char* lds, const float* codebook, int n, float scale) {
+    if constexpr (!PAIR) {
+      each_codeword(codebook, 1 << n, [&](int i, float c) {
+        Codeword<E>::write(reinterpret_cast<unsigned*>(lds) + i * kWords, c, scale);
+      });
+    } else {
+      // window i holds the states i >> K and i mod 2^n: those of one first state have neighbouring second ones
+      const unsigned states = 1u << n;
+#pragma unroll 4
+      for (unsigned s = threadIdx.x; s < states; s += blockDim.x) {
+        const float first = codebook[s];
+        const float* second = codebook + ((s << K) & (states - 1));
+        unsigned* at = reinterpret_cast<unsigned*>(lds) + (s << K) * kWords;
+#pragma unroll
+        for (int b = 0; b < 1 << K; ++b) {
+          Codeword<E>::write(at + b * kWords, first, scale);
+          Codeword<E>::write(at + b * kWords + Codeword<E>::kWords, second[b], scale);
+        }
+      }
+    }
+  }
+};
+
 // What a step of a wave reads.
-template <class E, int F, int RT, int NT, int K>
+template <class E, int F, int RT, int NT, int K, bool PAIR>
 struct CodeStep {
   using T = typename TileOf<E>::T;
   using V = typename T::V;
   using X = XTile<E, F, NT>;
+  using Tab = Table<E, K, PAIR>;
   static constexpr int kKept = Place<E, F>::kKept;
-  static constexpr int kParts = std::is_same<E, F32>::value ? 3 : 2;
   static constexpr int kShare = K <= 2 ? 8 : 4;  // states read from one 32-bit window: n + K (kShare - 1) <= 29
   X x;
   unsigned w[RT][K + 1];
-  float scale[RT];
+  float scale;
 
-  // co, so: a lane's offsets in the rows' codes and scales. With TAIL some of the step's folds are not there.
+  // In memory order: four neighbouring lanes load the K + 1 words each of four chunks of 32 weights, and lane
+  // (g, c16) the scale of tile g's row c16. co: a lane's offsets in the rows' codes, so: in the scales. With TAIL some
+  // of the step's folds are not there.
   template <bool TAIL>
   __device__ void load(const CodeArgs& a, const Place<E, F>& pl, int s, const unsigned* __restrict__ code,
-                       const unsigned (&co)[RT], const float* __restrict__ scales, const unsigned (&so)[RT],
+                       const unsigned (&co)[RT], const float* __restrict__ scales, unsigned so,
                        const typename X::Rows& rows) {
-    const int block = s * F + pl.fold;
-    const bool in = !TAIL || block * 128 < a.tile.cols;
-    int chain = divide(block, a.reciprocal);
-    const unsigned at = chain * a.words + (block - chain * a.per_chain) * (4 * K);
-    if (TAIL) chain = min(chain, a.chains - 1);
-    const bool more = a.n > K;  // the last of the K + 1 words is there
+    typedef unsigned Words __attribute__((ext_vector_type(K < 4 ? K + 1 : 4), aligned(4)));
+    {
+      const int block = s * F + ((threadIdx.x & 63) >> 2) % F, chain = divide(block, a.reciprocal);
+      const unsigned at = chain * a.words + (block - chain * a.per_chain) * (4 * K);
+      const bool in = !TAIL || block * 128 < a.tile.cols;
+      const bool more = a.n > K;  // the last of the K + 1 words is there
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
+      for (int t = 0; t < RT; ++t) {
+        const unsigned* p = code + co[t] + at;
 #pragma unroll
-      for (int i = 0; i <= K; ++i) w[t][i] = in && (i < K || more) ? code[co[t] + at + i] : 0u;
-      scale[t] = a.scales != nullptr ? scales[so[t] + chain] : 1.0f;
+        for (int i = 0; i <= K; ++i) w[t][i] = 0u;
+        if (in) {
+          if (K < 4 && more) {
+            const Words v = *reinterpret_cast<const Words*>(p);
+#pragma unroll
+            for (int i = 0; i <= K; ++i) w[t][i] = v[i < 4 ? i : 3];
+          } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i) w[t][i] = p[i];
+            if (more) w[t][K] = p[K];
+          }
+        }
+      }
     }
+    const int chain = divide(s * F + pl.fold, a.reciprocal);
+    scale = a.scales == nullptr ? 1.0f : pl.g < RT ? scales[so + (TAIL ? min(chain, a.chains - 1) : chain)] : 0.0f;
     x.template load<TAIL>(a.tile, rows, s);
   }
 
-  __device__ void add(const Place<E, F>& pl, char* lds, const char* table, int shift, unsigned mask,
-                      float (&acc)[RT][NT][kKept]) const {
+  // The words of weights 8 j .. 8 j + 7 of tile t.
+  __device__ void gather(int t, int j, const char* table, int shift, unsigned mask, unsigned (&e)[8 * Codeword<E>::kWords]) const {
+    constexpr int kStates = PAIR ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < 8; i += kStates) {
+      const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
+      const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
+      const auto v = *reinterpret_cast<const typename Tab::Entry*>(table + (window >> (shift - K * (i % kShare)) & mask));
+#pragma unroll
+      for (int k = 0; k < Tab::kWords; ++k) e[i * Codeword<E>::kWords + k] = v[k];
+    }
+  }
+
+  __device__ void add(const Place<E, F>& pl, const char* table, char* lds, int shift, unsigned mask,
+                      float (&acc)[RT][NT][kKept]) {
+    constexpr int kWords = Codeword<E>::kWords, kOps = 2 * kWords;  // operands of 8 weights
     x.put(lds);
-    V xo[NT][4];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int i = 0; i <= K; ++i) w[t][i] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][i]);
+    unsigned sc[RT];
+    rows_apart<RT>(__float_as_uint(scale), sc);
+    // x[i] twice (fp32: four times), for each word of weight i
+    V xo[NT][4][kOps];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xo[n][j] = X::get(lds, pl, n, 4 * pl.g + j);
-    X::in_order();
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      f32x4 d[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
       for (int j = 0; j < 4; ++j) {
-        unsigned e[8];
+        const u32x4 v = __builtin_bit_cast(u32x4, X::get(lds, pl, n, 4 * pl.g + j));
+        u32x4 twice[kOps];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
-          const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
-          e[i] = *reinterpret_cast<const unsigned*>(table + (window >> (shift - K * (i % kShare)) & mask));
-        }
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) d[n] = add_products<T, kParts>(e, xo[n][j], d[n]);
+          for (int k = 0; k < kWords; ++k)
+            twice[(i * kWords + k) / 4][(i * kWords + k) % 4] = __builtin_amdgcn_perm(v[i / 2], v[i / 2], i % 2 ? 0x03020302 : 0x01000100);
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) xo[n][j][o] = __builtin_bit_cast(V, twice[o]);
       }
+    X::in_order();
+    unsigned e[2][8 * kWords];
+    gather(0, 0, table, shift, mask, e[0]);
+    f32x4 d[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int tj = 0; tj < 4 * RT; ++tj) {  // the next eight weights are asked for before these are used
+      const int t = tj / 4, j = tj % 4;
+      if (tj + 1 < 4 * RT) gather((tj + 1) / 4, (tj + 1) % 4, table, shift, mask, e[(tj + 1) % 2]);
 #pragma unroll
-        for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(scale[t], pl.kept(d[n], u), acc[t][n][u]);
+      for (int n = 0; n < NT; ++n) {
+        if (j == 0) d[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) {
+          const unsigned* u = e[tj % 2] + 4 * o;
+          d[n] = T::mfma(xo[n][j][o], __builtin_bit_cast(V, u32x4{u[0], u[1], u[2], u[3]}), d[n]);
+        }
+      }
+      if (j == 3)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(__uint_as_float(sc[t]), pl.kept(d[n], u), acc[t][n][u]);
     }
   }
 };
 
 // F folds, RT tiles of rows and NT tiles of tokens a wave, K bits a step.
-template <class E, int F, int RT, int NT, int K>
+template <class E, int F, int RT, int NT, int K, bool PAIR>
 __global__ void __launch_bounds__(64 * kMaxWaves)
 k_code_tiles(const CodeArgs a) {
   using Pl = Place<E, F>;
@@ -174,49 +234,56 @@ k_code_tiles(const CodeArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int states = 1 << a.n;
   const Pl pl;
-  char* mine = lds + pl.wave * NT * kXBytes;
-  char* table = lds + pl.waves * NT * kXBytes;
-  const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(lds));
-  const float down = ldexpf(1.0f, -top), up = ldexpf(1.0f, top);
-  for (int i = threadIdx.x; i < states; i += blockDim.x)
-    reinterpret_cast<unsigned*>(table)[i] = Codeword<E>::entry(a.codebook[i], down);
-  __syncthreads();
-
+  using Tab = Table<E, K, PAIR>;
+  char* xs = lds + Tab::bytes(a.n);  // the waves' x, behind the table
+  char* mine = xs + pl.wave * NT * kXBytes;
   const int kw = a.tile.kw, ki = pl.wave % kw, ri = pl.wave / kw, rw = pl.waves / kw;
   const int whole = a.tile.cols / (F * 128), steps = whole + (whole * (F * 128) < a.tile.whole8() ? 1 : 0);
   const long long rows = a.tile.rows, units = (rows + RT * kRows - 1) / (RT * kRows);  // of rows, one for a wave
   const long long m0 = (long long)blockIdx.y * (NT * Pl::kTokens);
   const XRows<E, F, NT> xrows(a.tile, m0);
-  const unsigned mask = (unsigned)(states - 1) << 2;
-  const int shift = 30 - a.n;  // a state at the top of a window as the byte offset of its codeword
+  // a state, or two, at the top of a window as the byte offset of its entry
+  const int bits = a.n + (PAIR ? K : 0), shift = 32 - Tab::kShift - bits;
+  const unsigned mask = ((1u << bits) - 1u) << Tab::kShift;
 
-  for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
-    const long long row0 = (ub + ri) * (RT * kRows);
+  CodeStep<E, F, RT, NT, K, PAIR> one, two;
+  const unsigned* __restrict__ code;
+  const float* __restrict__ scales;
+  unsigned co[RT], so;
+  const int lane = threadIdx.x & 63;
+  auto load = [&](auto& step, int s) {
+    if (s < whole)
+      step.template load<false>(a, pl, s, code, co, scales, so, xrows);
+    else
+      step.template load<true>(a, pl, s, code, co, scales, so, xrows);
+  };
+  // A unit's first loads, before the table for the first one: it takes as long as they do.
+  auto begin = [&](long long unit) {
+    const long long row0 = unit * (RT * kRows);
     // offsets from the wave's first row fit 32 bits; rows behind the last repeat it
     const long long base = row0 < rows ? row0 : rows - 1;
     const int last = (int)(rows - 1 - base < RT * kRows ? rows - 1 - base : RT * kRows);
-    const unsigned* __restrict__ code = a.code + base * a.chains * a.words;
-    const float* __restrict__ scales = a.scales + base * a.chains;
-    unsigned co[RT], so[RT];
-    float acc[RT][NT][kKept] = {};
+    code = a.code + base * a.chains * a.words;
+    scales = a.scales + base * a.chains;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      so[t] = (unsigned)(min(t * kRows + pl.row(), last) * a.chains);
-      co[t] = so[t] * a.words + K * pl.g;
-    }
-    CodeStep<E, F, RT, NT, K> one, two;
-    auto load = [&](auto& step, int s) {
-      if (s < whole)
-        step.template load<false>(a, pl, s, code, co, scales, so, xrows);
-      else
-        step.template load<true>(a, pl, s, code, co, scales, so, xrows);
-    };
+    for (int t = 0; t < RT; ++t) co[t] = (unsigned)(min(t * kRows + (lane >> 2) / F, last) * a.chains * a.words + K * (lane & 3));
+    so = (unsigned)(min(min(pl.g, RT - 1) * kRows + pl.row(), last) * a.chains);
     if (ki < steps) load(one, ki);
+  };
+  begin((long long)blockIdx.x * rw + ri);
+  const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(xs));
+  const float down = ldexpf(1.0f, -top), up = ldexpf(1.0f, top);
+  Tab::make(lds, a.codebook, a.n, down);
+  __syncthreads();
+
+
+  for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
+    float acc[RT][NT][kKept] = {};
     for (int s = ki; s < steps; s += 2 * kw) {
       if (s + kw < steps) load(two, s + kw);
-      one.add(pl, mine, table, shift, mask, acc);
+      one.add(pl, lds, mine, shift, mask, acc);
       if (s + 2 * kw < steps) load(one, s + 2 * kw);
-      if (s + kw < steps) two.add(pl, mine, table, shift, mask, acc);
+      if (s + kw < steps) two.add(pl, lds, mine, shift, mask, acc);
     }
     if constexpr (std::is_same<E, F16>::value) {
 #pragma unroll
@@ -226,7 +293,8 @@ k_code_tiles(const CodeArgs a) {
 #pragma unroll
           for (int u = 0; u < kKept; ++u) acc[t][n][u] *= up;
     }
-    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, lds, [](long long, const typename E::T*) { return 0.0f; });
+    if (ub + (long long)gridDim.x * rw < units) begin(ub + (long long)gridDim.x * rw + ri);
+    join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, xs, [](long long, const typename E::T*) { return 0.0f; });
   }
 }
 

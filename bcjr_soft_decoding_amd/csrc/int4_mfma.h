@@ -41,24 +41,6 @@ __device__ inline typename T::V weights8(unsigned w, unsigned one) {
   return __builtin_bit_cast(typename T::V, v);
 }
 
-// v of the 16 lanes of row t, for every row of 16 lanes.
-template <int N>
-__device__ inline void rows_apart(unsigned v, unsigned (&out)[N]) {
-  if constexpr (N == 1) {
-    out[0] = v;
-  } else {
-    const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // rows 0 1 0 1, rows 2 3 2 3
-    const auto low = __builtin_amdgcn_permlane16_swap(halves[0], halves[0], false, false);
-    out[0] = low[0];
-    out[1] = low[1];
-    if constexpr (N > 2) {
-      const auto high = __builtin_amdgcn_permlane16_swap(halves[1], halves[1], false, false);
-      out[2] = high[0];
-      out[3] = high[1];
-    }
-  }
-}
-
 // What a step of a wave reads, in memory order: of a tile's codes a lane loads the 16 bytes next to its
 // neighbour's, and of the scales those of tile g.
 template <class E, int F, int RT, int NT, int GS, bool ZEROS>
@@ -88,19 +70,18 @@ struct Int4Step {
     for (int i = 0; i < kGroups; ++i) {
       int group = divide(unit + i * GS, a.per_group);
       if (TAIL) group = min(group, a.groups - 1);
-      scale[i] = scales[so + group];
-      if (ZEROS) zero[i] = zeros[so + group];
+      scale[i] = pl.g < RT ? scales[so + group] : 0.0f;
+      if (ZEROS) zero[i] = pl.g < RT ? zeros[so + group] : 0u;
     }
     x.template load<TAIL>(a.tile, rows, s);
   }
 
   __device__ void add(const Place<E, F>& pl, char* lds, float (&acc)[RT][NT][kKept]) {
     x.put(lds);
-    const int from = (4 * pl.c16 + pl.g) * 4;  // the lane that loaded this one's codes
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[t][j] = __builtin_amdgcn_ds_bpermute(from, w[t][j]);
+      for (int j = 0; j < 4; ++j) w[t][j] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][j]);
     V xo[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)

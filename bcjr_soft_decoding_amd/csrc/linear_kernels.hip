@@ -4,10 +4,10 @@
 // c(s_t) x[m, q L + t].
 #include <hip/hip_runtime.h>
 
-#include "code_mfma.h"
 #include "internal.h"
 #include "ops.h"
 #include "ops_device.h"
+#include "tiles.h"
 
 namespace bcjr {
 namespace {
@@ -46,62 +46,14 @@ k_code_matvec(const unsigned* __restrict__ code, long long rows, long long cols,
   }
 }
 
-template <class E, int F, int RT, int NT, int K>
-int launch_tiles(CodeArgs a, hipStream_t stream) {
-  constexpr int kRowsOfWave = RT * 16 / F;
-  const int steps = (a.tile.cols / 128 + F - 1) / F;
-  const int64_t units = (a.tile.rows + kRowsOfWave - 1) / kRowsOfWave;
-  // Every block makes a table: 8 waves share it, or as many as LDS leaves room for beside it (4 at 2^15
-  // states), and no more blocks than fit the chip are started.
-  auto lds_of = [&](int waves) { return ((size_t)1 << a.n) * sizeof(float) + (size_t)waves * NT * kXBytes; };
-  int waves = kMaxWaves;
-  while (lds_of(waves) > kLds) waves /= 2;
-  const size_t lds = lds_of(waves);
-  const int along = waves_along(steps, units), kw = along < waves ? along : waves;
-  a.tile.kw = kw;
-  const int64_t rw = waves / kw, blocks = (units + rw - 1) / rw;
-  const int64_t tokens = (a.tile.tokens + NT * tile_tokens<E, F>() - 1) / (NT * tile_tokens<E, F>());
-  const void* kernel = reinterpret_cast<const void*>(k_code_tiles<E, F, RT, NT, K>);
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return (int)e;
-  }
-  const int64_t room = 256 * (lds > kLds / 2 ? 1 : 2);
-  hipLaunchKernelGGL((k_code_tiles<E, F, RT, NT, K>), dim3((unsigned)(blocks < room ? blocks : room), (unsigned)tokens),
-                     dim3(64 * waves), lds, stream, a);
-  return (int)hipGetLastError();
-}
-
-template <class E, int F, int RT, int NT>
-int launch_tiles_bits(const CodeArgs& a, int k, hipStream_t stream) {
-  return k == 1   ? launch_tiles<E, F, RT, NT, 1>(a, stream)
-         : k == 2 ? launch_tiles<E, F, RT, NT, 2>(a, stream)
-         : k == 3 ? launch_tiles<E, F, RT, NT, 3>(a, stream)
-                  : launch_tiles<E, F, RT, NT, 4>(a, stream);
-}
-
-// The largest fold that the tokens leave room for and the columns fill.
-template <class E>
-int launch_tiles_any(const CodeArgs& a, int k, hipStream_t stream) {
-  const int blocks = a.tile.cols / 128;
-  if constexpr (TileOf<E>::T::kParts == 1) {
-    if (a.tile.tokens == 1 && blocks > 8) return launch_tiles_bits<E, 16, 2, 1>(a, k, stream);
-    if (a.tile.tokens <= 2 && blocks > 4) return launch_tiles_bits<E, 8, 2, 1>(a, k, stream);
-  }
-  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_tiles_bits<E, 4, 2, 1>(a, k, stream);
-  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_tiles_bits<E, 2, 1, 1>(a, k, stream);
-  // beside 2^15 codewords there is no room for the x of two tiles of tokens
-  if (a.tile.tokens <= tile_tokens<E, 1>() || a.n == 15) return launch_tiles_bits<E, 1, 1, 1>(a, k, stream);
-  return launch_tiles_bits<E, 1, 1, 2>(a, k, stream);
-}
-
 }  // namespace
 
 int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t cols, int64_t L,
                        const float* codebook, const float* scales, const MatvecIO& io, void* stream) {
-  // The matrix-core form: whole blocks of 128 columns in a chain and a table that fits LDS.
+  // The matrix-core form: whole blocks of 128 columns in a chain and a table of at most 128 KiB, which leaves 8 waves
+  // the LDS they need (a codeword takes 4 bytes, 8 for fp32).
   const int64_t words = code_words(n, k, L);
-  if (L % 128 == 0 && n <= 15 && k <= 4 && cols <= kTileColumns) {
+  if (L % 128 == 0 && n <= (io.dtype == BCJR_F32 ? 14 : 15) && k <= 4 && cols <= kTileColumns) {
     CodeArgs a;
     a.code = code;
     a.codebook = codebook;
@@ -113,9 +65,9 @@ int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t
     a.reciprocal = 1.0f / (float)a.per_chain;
     return in_pieces(io, io.dtype == BCJR_F32 ? 4 : 2, [&](const MatvecIO& piece) {
       a.tile = tile_args(piece, rows, cols);
-      return with_type(io.dtype, [&](auto e) {
-        return launch_tiles_any<decltype(e)>(a, k, static_cast<hipStream_t>(stream));
-      });
+      return io.dtype == BCJR_F32   ? launch_code_tiles_f32(a, k, stream)
+             : io.dtype == BCJR_F16 ? launch_code_tiles_f16(a, k, stream)
+                                    : launch_code_tiles_bf16(a, k, stream);
     });
   }
   return with_type(io.dtype, [&](auto e) {

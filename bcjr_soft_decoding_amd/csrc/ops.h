@@ -18,6 +18,13 @@ struct MatvecIO {
 
 int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t cols, int64_t L,
                        const float* codebook, const float* scales, const MatvecIO& io, void* stream);
+
+// The tiled products with trellis-coded weights, one type each (code_tiles.hip, built once for each).
+struct CodeArgs;
+int launch_code_tiles_f32(const CodeArgs& a, int k, void* stream);
+int launch_code_tiles_f16(const CodeArgs& a, int k, void* stream);
+int launch_code_tiles_bf16(const CodeArgs& a, int k, void* stream);
+
 int launch_int4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, int64_t group,
                          uint32_t* q, float* scales, uint8_t* zeros, void* stream);
 int launch_int4_dequantize(const uint32_t* q, const float* scales, const uint8_t* zeros,

@@ -30,6 +30,16 @@ struct TileArgs {
   __host__ __device__ int whole8() const { return cols & ~7; }
 };
 
+struct CodeArgs {
+  TileArgs tile;
+  const unsigned* code;
+  const float* codebook;
+  const float* scales;         // of a chain, or NULL
+  int n, chains, words;        // state bits; chains of a row; words of a chain
+  int per_chain;               // blocks of 128 columns in a chain
+  float reciprocal;            // 1 / per_chain
+};
+
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -98,6 +108,9 @@ struct Place {
     fold = c16 % F;
     col = c16 / F;
   }
+  // The lane that loaded this one's codes, for ds_bpermute: four neighbouring lanes load what four lanes of one row
+  // of the tile, 16 apart, need.
+  __device__ int from() const { return (4 * c16 + g) * 4; }
   // Row of W in the tile, of a lane's weights and of its sums.
   __device__ int row() const { return c16 / F; }
   // Row of x, without folds, of kept sum u: the lane holds the sums of the tile's rows 4 g + i of x, and keeps
@@ -115,12 +128,28 @@ struct Place {
   }
 };
 
+// v of the 16 lanes of row t, for every row of 16 lanes: what lane (t, c16) loaded for the rows of tile t.
+template <int N>
+__device__ inline void rows_apart(unsigned v, unsigned (&out)[N]) {
+  const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // rows 0 1 0 1, rows 2 3 2 3
+  const auto low = __builtin_amdgcn_permlane16_swap(halves[0], halves[0], false, false);
+  out[0] = low[0];
+  if constexpr (N > 1) out[1] = low[1];
+  if constexpr (N > 2) {
+    const auto high = __builtin_amdgcn_permlane16_swap(halves[1], halves[1], false, false);
+    out[2] = high[0];
+    out[3] = high[1];
+  }
+}
+
 // The x of one step of a wave, NT tiles of 16 rows of 128 columns. Neighbouring lanes load neighbouring
 // memory, 16 lanes a row: in the operands' own order every lane of a load would be in a row, and so a
 // cache line, of its own, and take a cycle of the cache instead of a quarter. The rows then go through LDS
 // (each wave its own kXBytes NT), where operands are read.
-constexpr int kXStride = 256 + 16;        // bytes of a row: 8 lanes that read one chunk of 8 rows meet no bank twice
-constexpr int kXBytes = 16 * kXStride;
+constexpr int kXBytes = 16 * 256;
+// Place of chunk c (16 bytes) of row r: shifted about by the row, so that neither the 16 chunks of a row nor one
+// chunk of eight rows meet a bank twice.
+__device__ inline int x_place(int r, int c) { return r * 256 + (c ^ r) * 16; }
 
 // Where a lane's loads begin, from the first token's row on (in_pieces() sees to it that 32 bits hold that):
 // rows behind the last token repeat it (their sums are not kept).
@@ -175,9 +204,9 @@ struct XTile {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = 4 * i + (lane >> 4);
-        char* at = lds + n * kXBytes + (lane & 15) * 16;
+        char* at = lds + n * kXBytes;
         if constexpr (kParts == 1) {
-          *reinterpret_cast<V*>(at + r * kXStride) = raw[n][i];
+          *reinterpret_cast<V*>(at + x_place(r, lane & 15)) = raw[n][i];
         } else {
           // three bfloat16 that add up to x: its leading 8 bits, the next 8 and the rest
           u32x4 part[3];
@@ -199,14 +228,14 @@ struct XTile {
           if (kLoads * 4 == kTokens * F || r < kTokens * F)
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-              *reinterpret_cast<u32x4*>(at + ((r / F * 3 + p) * F + r % F) * kXStride) = part[p];
+              *reinterpret_cast<u32x4*>(at + x_place((r / F * 3 + p) * F + r % F, lane & 15)) = part[p];
         }
       }
     in_order();
   }
   // The operand of a lane from chunk `chunk` (8 columns) of its row.
   static __device__ V get(const char* lds, const Place<E, F>& pl, int n, int chunk) {
-    return *reinterpret_cast<const V*>(lds + n * kXBytes + pl.c16 * kXStride + chunk * 16);
+    return *reinterpret_cast<const V*>(lds + n * kXBytes + x_place(pl.c16, chunk));
   }
   // Lanes of a wave read what others wrote: LDS works in order, the compiler has to as well.
   static __device__ void in_order() {

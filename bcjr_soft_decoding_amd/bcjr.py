@@ -147,7 +147,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of
 
 def _stream(device):
     if _raw_stream is not None and device.index is not None:
-        return ctypes.c_void_p(_raw_stream(device.index))
+        return _raw_stream(device.index)
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -560,6 +560,7 @@ def bcjr_unpack_code(code, n, k, L, codebook=None, states=None, w_hard=None):
 # ---- products with quantised weights -------------------------------------------------------------
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_Tensor = torch.Tensor
 U8 = torch.uint8
 
 
@@ -575,6 +576,8 @@ def _dtype_code(t, name):
 def _rows2(t, name, dtype, shape):
     """t must be a matrix of this dtype and shape (None = any size) whose rows are contiguous;
     returns the elements between its rows."""
+    if type(t) is torch.Tensor and t.dtype == dtype and t.dim() == 2 and shape[0] is None and t.is_contiguous():
+        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -603,22 +606,35 @@ def _product_x(x):
     return code, tokens, cols, stride
 
 
-def _product_y(x, y, tokens, rows, dev):
-    """The output of a product and its row stride: the caller's, checked, or a new one."""
-    if y is None:
-        return x.new_empty((tokens, rows)), rows
-    if y.device != dev:
-        raise ValueError(f"tensors on {dev} and {y.device}: a call runs on one device")
-    return y, _rows2(y, "y", x.dtype, (tokens, rows))
-
-
 def bcjr_code_matvec(x, code, codebook, n, k, L, scales=None, y=None):
     """Products y [tokens, rows] = x [tokens, cols] W^T with trellis-coded weights: uint32 codes
     [rows cols / L, words] of the chains cut row-major from W, optionally a fp32 scale for each."""
-    dt, tokens, cols, xs = _product_x(x)
+    # as in bcjr_int4_matvec: the everyday call first
+    if not (type(x) is _Tensor and type(code) is _Tensor and type(codebook) is _Tensor and y is None
+            and (scales is None or (type(scales) is _Tensor and scales.dtype is F32 and scales.is_contiguous()
+                                    and scales.device == x.device))
+            and type(n) is int and type(k) is int and type(L) is int and 1 <= k <= n <= 16 and L > 0
+            and x.dim() == 2 and x.is_contiguous() and not x.requires_grad and x.dtype in DTYPES
+            and code.dtype is U32 and code.is_contiguous() and codebook.dtype is F32 and codebook.is_contiguous()
+            and x.device == code.device == codebook.device and x.is_cuda):
+        return _code_matvec_checked(x, code, codebook, n, k, L, scales, y)
+    tokens, cols = x.shape
+    B = code.shape[0]
+    if (cols < 1 or cols % L or B % (cols // L) or code.shape != (B, (n + k * (L - 1) + 31) // 32)
+            or codebook.shape != (1 << n,) or (scales is not None and scales.shape != (B,))):
+        return _code_matvec_checked(x, code, codebook, n, k, L, scales, y)
+    rows = B // (cols // L)
+    y = x.new_empty((tokens, rows))
+    return _code_matvec_call(x, code, codebook, n, k, L, scales, rows, tokens, cols, cols, y, rows)
+
+
+def _code_matvec_checked(x, code, codebook, n, k, L, scales, y):
+    _, tokens, cols, xs = _product_x(x)
+    if code is None or codebook is None:
+        raise ValueError("code and codebook are required")
     B, nw = _chains2(code, "code", U32)
     n, k, L = int(n), int(k), int(L)
-    words = (n + k * (L - 1) + 31) // 32 if L > 0 and 1 <= k <= n <= 16 else 0
+    words = bcjr_code_words(n, k, L)
     if words == 0 or nw != words:
         raise ValueError(f"code has {nw} words per chain; n={n}, k={k}, L={L} need {words}")
     if cols < 1 or cols % L or B % (cols // L):
@@ -626,16 +642,21 @@ def bcjr_code_matvec(x, code, codebook, n, k, L, scales=None, y=None):
     rows = B // (cols // L)
     _spec(codebook, "codebook", F32, (1 << n,))
     _spec(scales, "scales", F32, (B,))
-    if y is not None:
-        _rows2(y, "y", x.dtype, (tokens, rows))
-    dev = _device(x, code, codebook, scales)
-    y, ys = _product_y(x, y, tokens, rows, dev)
+    ys = rows if y is None else _rows2(y, "y", x.dtype, (tokens, rows))
+    _device(x, code, codebook, scales, y)
+    y = x.new_empty((tokens, rows)) if y is None else y
+    return _code_matvec_call(x, code, codebook, n, k, L, scales, rows, tokens, cols, xs, y, ys)
+
+
+def _code_matvec_call(x, code, codebook, n, k, L, scales, rows, tokens, cols, xs, y, ys):
+    dev = x.device
     tr = Trellis(n, k, 1, codebook.data_ptr())
     with _on(dev):
         st = lib().bcjr_code_matvec(ctypes.byref(tr), code.data_ptr(), rows, cols, L,
-                                    None if scales is None else scales.data_ptr(), x.data_ptr(), tokens, xs, dt,
-                                    y.data_ptr(), ys, _stream(dev))
-    _check(st, "bcjr_code_matvec")
+                                    None if scales is None else scales.data_ptr(), x.data_ptr(), tokens, xs,
+                                    DTYPES[x.dtype], y.data_ptr(), ys, _stream(dev))
+    if st:
+        _check(st, "bcjr_code_matvec")
     return y
 
 
@@ -672,15 +693,20 @@ def bcjr_int4_quantize(w, group, with_zeros=False):
 
 def _int4_weights(q, scales, zeros, cols, group):
     """Checks 4-bit weights against their number of columns; returns their rows."""
-    rows, nw = _chains2(q, "q", U32)
+    if q is None:
+        raise ValueError("q is required")
+    _spec(q, "q", U32, None)
+    if q.dim() != 2:
+        raise ValueError(f"q must have shape [rows, words], got {tuple(q.shape)}")
+    rows, nw = q.shape
     words = bcjr_int4_words(cols)
-    if nw != words:
+    if cols < 1 or nw != words:
         raise ValueError(f"q has {nw} words in a row; {cols} columns need {words}")
-    groups = -(-cols // group)
-    _spec(scales, "scales", F32, (rows, groups))
     if scales is None:
         raise ValueError("scales are required")
-    _spec(zeros, "zeros", U8, (rows, groups))
+    shape = (rows, -(-cols // group))
+    _spec(scales, "scales", F32, shape)
+    _spec(zeros, "zeros", U8, shape)
     return rows
 
 
@@ -700,17 +726,41 @@ def bcjr_int4_dequantize(q, scales, zeros, cols, group, w=None):
 
 def bcjr_int4_matvec(x, q, scales, zeros, group, y=None):
     """Products y [tokens, rows] = x [tokens, cols] W^T with 4-bit weights."""
-    dt, tokens, cols, xs = _product_x(x)
+    # One token is a few microseconds of GPU time, so the checks are ordered by cost: what an everyday call passes
+    # is compared in place, and only a call that fails that is looked at in detail.
+    if not (type(x) is _Tensor and type(q) is _Tensor and type(scales) is _Tensor and zeros is None and y is None
+            and x.dim() == 2 and x.is_contiguous() and not x.requires_grad and x.dtype in DTYPES
+            and q.dtype is U32 and q.is_contiguous() and scales.dtype is F32 and scales.is_contiguous()
+            and type(group) is int and group > 0 and group % 32 == 0
+            and x.device == q.device == scales.device and x.is_cuda):
+        return _int4_matvec_checked(x, q, scales, zeros, group, y)
+    tokens, cols = x.shape
+    words = (cols + 127) // 128 * 16
+    rows = q.shape[0]
+    if cols < 1 or q.shape != (rows, words) or scales.shape != (rows, -(-cols // group)):
+        return _int4_matvec_checked(x, q, scales, zeros, group, y)
+    y = x.new_empty((tokens, rows))
+    return _int4_matvec_call(x, q, scales, None, rows, cols, group, tokens, cols, y, rows)
+
+
+def _int4_matvec_checked(x, q, scales, zeros, group, y):
+    _, tokens, cols, xs = _product_x(x)
     group = _group(group)
     rows = _int4_weights(q, scales, zeros, cols, group)
-    if y is not None:
-        _rows2(y, "y", x.dtype, (tokens, rows))
-    dev = _device(x, q, scales, zeros)
-    y, ys = _product_y(x, y, tokens, rows, dev)
+    ys = rows if y is None else _rows2(y, "y", x.dtype, (tokens, rows))
+    _device(x, q, scales, zeros, y)
+    y = x.new_empty((tokens, rows)) if y is None else y
+    return _int4_matvec_call(x, q, scales, zeros, rows, cols, group, tokens, xs, y, ys)
+
+
+def _int4_matvec_call(x, q, scales, zeros, rows, cols, group, tokens, xs, y, ys):
+    dev = x.device
     with _on(dev):
         st = lib().bcjr_int4_matvec(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-                                    rows, cols, group, x.data_ptr(), tokens, xs, dt, y.data_ptr(), ys, _stream(dev))
-    _check(st, "bcjr_int4_matvec")
+                                    rows, cols, group, x.data_ptr(), tokens, xs, DTYPES[x.dtype], y.data_ptr(), ys,
+                                    _stream(dev))
+    if st:
+        _check(st, "bcjr_int4_matvec")
     return y
 
 

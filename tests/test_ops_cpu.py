@@ -121,6 +121,8 @@ def test_binding_refusals_int4():
     raises(lambda: f(scales=torch.zeros(4, 3)), "scales", "shape")
     raises(lambda: f(scales=None), "scales")
     raises(lambda: f(scales=s.half()), "scales", "float32")
+    raises(lambda: f(q=None), "q")
+    raises(lambda: f(x=[1.0]), "x")
     raises(lambda: f(zeros=torch.zeros(4, 4)), "zeros", "uint8")
     raises(lambda: f(group=40), "group")
     raises(lambda: f(y=torch.zeros(2, 5)), "y", "shape")
@@ -145,6 +147,9 @@ def test_binding_refusals_code():
     raises(lambda: f(y=torch.zeros(4, 2).t()), "y", "contiguous")
     raises(lambda: f(y=torch.zeros(3, 4)), "y", "shape")
     raises(lambda: f(L=0), "words")
+    raises(lambda: f(codebook=None), "codebook")
+    raises(lambda: f(code=None), "code")
+    raises(lambda: f(x=None), "x")
     raises(lambda: f(), "CUDA")
 
 

@@ -160,31 +160,59 @@ struct CodeStep {
     x.template load<TAIL>(a.tile, rows, s);
   }
 
-  // The words of weights 8 j .. 8 j + 7 of tile t.
-  __device__ void gather(int t, int j, const char* table, int shift, unsigned mask, unsigned (&e)[8 * Codeword<E>::kWords]) const {
-    constexpr int kStates = PAIR ? 2 : 1;
-#pragma unroll
-    for (int i = 0; i < 8; i += kStates) {
-      const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
-      const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
-      const auto v = *reinterpret_cast<const typename Tab::Entry*>(table + (window >> (shift - K * (i % kShare)) & mask));
-#pragma unroll
-      for (int k = 0; k < Tab::kWords; ++k) e[i * Codeword<E>::kWords + k] = v[k];
-    }
-  }
+  // What the products take, from what was loaded: its registers are free for the next step's loads then.
+  struct Operands {
+    static constexpr int kWords = Codeword<E>::kWords, kOps = 2 * kWords;  // operands of 8 weights
+    V x[NT][4][kOps];  // x[i] twice (fp32: four times), for each word of weight i
+    unsigned w[RT][K + 1], scale[RT];
 
-  __device__ void add(const Place<E, F>& pl, const char* table, char* lds, int shift, unsigned mask,
-                      float (&acc)[RT][NT][kKept]) {
-    constexpr int kWords = Codeword<E>::kWords, kOps = 2 * kWords;  // operands of 8 weights
+    // The words of weights 8 j .. 8 j + 7 of tile t.
+    __device__ void gather(int t, int j, const char* table, int shift, unsigned mask, unsigned (&e)[8 * kWords]) const {
+      constexpr int kStates = PAIR ? 2 : 1;
+#pragma unroll
+      for (int i = 0; i < 8; i += kStates) {
+        const int p = K * (8 * j + i / kShare * kShare), q = p / 32, r = p % 32;
+        const unsigned window = r == 0 ? w[t][q] : __builtin_amdgcn_alignbit(w[t][q], w[t][q + 1], 32 - r);
+        const auto v = *reinterpret_cast<const typename Tab::Entry*>(table + (window >> (shift - K * (i % kShare)) & mask));
+#pragma unroll
+        for (int k = 0; k < Tab::kWords; ++k) e[i * kWords + k] = v[k];
+      }
+    }
+
+    __device__ void add(const Place<E, F>& pl, const char* table, int shift, unsigned mask, float (&acc)[RT][NT][kKept]) const {
+      unsigned e[2][8 * kWords];
+      gather(0, 0, table, shift, mask, e[0]);
+      f32x4 d[NT];
+#pragma unroll
+      for (int tj = 0; tj < 4 * RT; ++tj) {  // the next eight weights are asked for before these are used
+        const int t = tj / 4, j = tj % 4;
+        if (tj + 1 < 4 * RT) gather((tj + 1) / 4, (tj + 1) % 4, table, shift, mask, e[(tj + 1) % 2]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (j == 0) d[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int o = 0; o < kOps; ++o) {
+            const unsigned* u = e[tj % 2] + 4 * o;
+            d[n] = T::mfma(x[n][j][o], __builtin_bit_cast(V, u32x4{u[0], u[1], u[2], u[3]}), d[n]);
+          }
+        }
+        if (j == 3)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(__uint_as_float(scale[t]), pl.kept(d[n], u), acc[t][n][u]);
+      }
+    }
+  };
+
+  __device__ void exchange(const Place<E, F>& pl, char* lds, Operands& o) const {
+    constexpr int kWords = Operands::kWords, kOps = Operands::kOps;
     x.put(lds);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int i = 0; i <= K; ++i) w[t][i] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][i]);
-    unsigned sc[RT];
-    rows_apart<RT>(__float_as_uint(scale), sc);
-    // x[i] twice (fp32: four times), for each word of weight i
-    V xo[NT][4][kOps];
+      for (int i = 0; i <= K; ++i) o.w[t][i] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][i]);
+    rows_apart<RT>(__float_as_uint(scale), o.scale);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -197,31 +225,9 @@ struct CodeStep {
           for (int k = 0; k < kWords; ++k)
             twice[(i * kWords + k) / 4][(i * kWords + k) % 4] = __builtin_amdgcn_perm(v[i / 2], v[i / 2], i % 2 ? 0x03020302 : 0x01000100);
 #pragma unroll
-        for (int o = 0; o < kOps; ++o) xo[n][j][o] = __builtin_bit_cast(V, twice[o]);
+        for (int p = 0; p < kOps; ++p) o.x[n][j][p] = __builtin_bit_cast(V, twice[p]);
       }
     X::in_order();
-    unsigned e[2][8 * kWords];
-    gather(0, 0, table, shift, mask, e[0]);
-    f32x4 d[NT];
-#pragma unroll
-    for (int tj = 0; tj < 4 * RT; ++tj) {  // the next eight weights are asked for before these are used
-      const int t = tj / 4, j = tj % 4;
-      if (tj + 1 < 4 * RT) gather((tj + 1) / 4, (tj + 1) % 4, table, shift, mask, e[(tj + 1) % 2]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (j == 0) d[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int o = 0; o < kOps; ++o) {
-          const unsigned* u = e[tj % 2] + 4 * o;
-          d[n] = T::mfma(xo[n][j][o], __builtin_bit_cast(V, u32x4{u[0], u[1], u[2], u[3]}), d[n]);
-        }
-      }
-      if (j == 3)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int u = 0; u < kKept; ++u) acc[t][n][u] = fmaf(__uint_as_float(sc[t]), pl.kept(d[n], u), acc[t][n][u]);
-    }
   }
 };
 
@@ -246,12 +252,13 @@ k_code_tiles(const CodeArgs a) {
   const int bits = a.n + (PAIR ? K : 0), shift = 32 - Tab::kShift - bits;
   const unsigned mask = ((1u << bits) - 1u) << Tab::kShift;
 
-  CodeStep<E, F, RT, NT, K, PAIR> one, two;
+  using Step = CodeStep<E, F, RT, NT, K, PAIR>;
+  Step step;
   const unsigned* __restrict__ code;
   const float* __restrict__ scales;
   unsigned co[RT], so;
   const int lane = threadIdx.x & 63;
-  auto load = [&](auto& step, int s) {
+  auto load = [&](int s) {
     if (s < whole)
       step.template load<false>(a, pl, s, code, co, scales, so, xrows);
     else
@@ -268,7 +275,7 @@ k_code_tiles(const CodeArgs a) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) co[t] = (unsigned)(min(t * kRows + (lane >> 2) / F, last) * a.chains * a.words + K * (lane & 3));
     so = (unsigned)(min(min(pl.g, RT - 1) * kRows + pl.row(), last) * a.chains);
-    if (ki < steps) load(one, ki);
+    if (ki < steps) load(ki);
   };
   begin((long long)blockIdx.x * rw + ri);
   const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(xs));
@@ -279,11 +286,11 @@ k_code_tiles(const CodeArgs a) {
 
   for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
     float acc[RT][NT][kKept] = {};
-    for (int s = ki; s < steps; s += 2 * kw) {
-      if (s + kw < steps) load(two, s + kw);
-      one.add(pl, lds, mine, shift, mask, acc);
-      if (s + 2 * kw < steps) load(one, s + 2 * kw);
-      if (s + kw < steps) two.add(pl, lds, mine, shift, mask, acc);
+    for (int s = ki; s < steps; s += kw) {
+      typename Step::Operands o;
+      step.exchange(pl, mine, o);
+      if (s + kw < steps) load(s + kw);
+      o.add(pl, lds, shift, mask, acc);
     }
     if constexpr (std::is_same<E, F16>::value) {
 #pragma unroll

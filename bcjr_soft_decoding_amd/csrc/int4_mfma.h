@@ -41,7 +41,7 @@ __device__ inline typename T::V weights8(unsigned w, unsigned one) {
   return __builtin_bit_cast(typename T::V, v);
 }
 
-// What a step of a wave reads, in memory order: of a tile's codes a lane loads the 16 bytes next to its
+// What a step of a wave reads, asked for while the one before is computed, in memory order: of a tile's codes a lane loads the 16 bytes next to its
 // neighbour's, and of the scales those of tile g.
 template <class E, int F, int RT, int NT, int GS, bool ZEROS>
 struct Int4Step {
@@ -76,51 +76,62 @@ struct Int4Step {
     x.template load<TAIL>(a.tile, rows, s);
   }
 
-  __device__ void add(const Place<E, F>& pl, char* lds, float (&acc)[RT][NT][kKept]) {
+  // What the products take, from what was loaded: its registers are free for the next step's loads then.
+  struct Operands {
+    V x[NT][4];
+    unsigned w[RT][4];
+    unsigned scale[kGroups][RT], zero[kGroups][RT];
+
+    __device__ void add(const Place<E, F>& pl, float (&acc)[RT][NT][kKept]) const {
+      unsigned one = T::kOne;
+      asm("" : "+v"(one));  // kept in a vector register
+      const V ones = __builtin_bit_cast(V, u32x4{one, one, one, one});
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        f32x4 sum[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          sum[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int j = i * GS; j < i * GS + GS; ++j) sum[n] = T::mfma(x[n][j], ones, sum[n]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          f32x4 d[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int j = i * GS; j < i * GS + GS; ++j) {
+            const V wj = weights8<T>(w[t][j], one);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) d[n] = T::mfma(x[n][j], wj, d[n]);
+          }
+          const float z = ZEROS ? fmaf((float)zero[i][t], 0.0625f, 1.0f) : 1.5f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < kKept; ++u)
+              acc[t][n][u] = fmaf(__uint_as_float(scale[i][t]), fmaf(-z, pl.kept(sum[n], u), pl.kept(d[n], u)), acc[t][n][u]);
+        }
+      }
+    }
+  };
+
+  __device__ void exchange(const Place<E, F>& pl, char* lds, Operands& o) const {
     x.put(lds);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[t][j] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][j]);
-    V xo[NT][4];
+      for (int j = 0; j < 4; ++j) o.w[t][j] = __builtin_amdgcn_ds_bpermute(pl.from(), w[t][j]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xo[n][j] = X::get(lds, pl, n, 4 * j + pl.g);
+      for (int j = 0; j < 4; ++j) o.x[n][j] = X::get(lds, pl, n, 4 * j + pl.g);
     X::in_order();
-    unsigned one = T::kOne;
-    asm("" : "+v"(one));  // kept in a vector register
-    const V ones = __builtin_bit_cast(V, u32x4{one, one, one, one});
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      f32x4 sum[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        sum[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = i * GS; j < i * GS + GS; ++j) sum[n] = T::mfma(xo[n][j], ones, sum[n]);
-      }
-      unsigned sc[RT], ze[RT];
-      rows_apart<RT>(__float_as_uint(scale[i]), sc);
-      if (ZEROS) rows_apart<RT>(zero[i], ze);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        f32x4 d[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = i * GS; j < i * GS + GS; ++j) {
-          const V wj = weights8<T>(w[t][j], one);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) d[n] = T::mfma(xo[n][j], wj, d[n]);
-        }
-        const float z = ZEROS ? fmaf((float)ze[t], 0.0625f, 1.0f) : 1.5f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int u = 0; u < kKept; ++u)
-            acc[t][n][u] = fmaf(__uint_as_float(sc[t]), fmaf(-z, pl.kept(sum[n], u), pl.kept(d[n], u)), acc[t][n][u]);
-      }
+      rows_apart<RT>(__float_as_uint(scale[i]), o.scale[i]);
+      if (ZEROS) rows_apart<RT>(zero[i], o.zero[i]);
     }
   }
 };
@@ -155,19 +166,20 @@ k_int4_tiles(const Int4Args a) {
     for (int t = 0; t < RT; ++t)
       qo[t] = (unsigned)(min(t * kRows + (lane >> 2) / F, last) * a.words + (lane >> 2) % F * 16 + 4 * (lane & 3));
     const unsigned so = (unsigned)(min(min(pl.g, RT - 1) * kRows + pl.row(), last) * a.groups);
-    Int4Step<E, F, RT, NT, GS, ZEROS> one, two;
-    auto load = [&](auto& step, int s) {
+    using Step = Int4Step<E, F, RT, NT, GS, ZEROS>;
+    Step step;
+    auto load = [&](int s) {
       if (s < whole)
         step.template load<false>(a, pl, s, q, qo, scales, zeros, so, xrows);
       else
         step.template load<true>(a, pl, s, q, qo, scales, zeros, so, xrows);
     };
-    if (ki < steps) load(one, ki);
-    for (int s = ki; s < steps; s += 2 * kw) {
-      if (s + kw < steps) load(two, s + kw);
-      one.add(pl, mine, acc);
-      if (s + 2 * kw < steps) load(one, s + 2 * kw);
-      if (s + kw < steps) two.add(pl, mine, acc);
+    if (ki < steps) load(ki);
+    for (int s = ki; s < steps; s += kw) {
+      typename Step::Operands o;
+      step.exchange(pl, mine, o);
+      if (s + kw < steps) load(s + kw);
+      o.add(pl, acc);
     }
     // codes were sixteenths
 #pragma unroll

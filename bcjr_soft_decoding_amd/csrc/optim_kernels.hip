@@ -43,8 +43,11 @@ __host__ __device__ inline unsigned mix(unsigned x) {
   return x ^ (x >> 16);
 }
 
-__device__ inline unsigned dither_bits(long long at, unsigned key) {
-  return mix((unsigned)at * 0x9E3779B1u + (unsigned)((unsigned long long)at >> 32) * 0x85EBCA6Bu + key);
+// What the dither of element `at` mixes; that of the next element is kDitherStep more (at is a multiple of 4, so four of
+// them have the same upper half).
+constexpr unsigned kDitherStep = 0x9E3779B1u;
+__device__ inline unsigned dither_seed(long long at, unsigned key) {
+  return (unsigned)at * kDitherStep + (unsigned)((unsigned long long)at >> 32) * 0x85EBCA6Bu + key;
 }
 
 __device__ inline float new_param(float p, float m, float r, const Hyper& h) {
@@ -52,29 +55,39 @@ __device__ inline float new_param(float p, float m, float r, const Hyper& h) {
   return fmaf(-h.rate, by, fmaf(-h.decay, p, p));
 }
 
-// floor(log2 |x|) of a finite x from the upper half of its bits, far below any other for zero and for
-// what is not finite. (No x is a subnormal double but by betas below 2^-800.)
-__device__ inline int exponent(int hi) {
-  const int e = (hi >> 20) & 0x7ff;
-  return e == 0 || e == 0x7ff ? -2000 : e - 1023;
+// A moment that is not finite, from the upper half of its bits.
+constexpr int kNotFinite = 0x7ff00000;
+
+// Byte b of a block whose largest finite magnitude has these upper bits: its exponent less 7, in 0 .. 254. (No moment is
+// a subnormal double but by betas below 2^-800; they count as zero.)
+__device__ inline int block_exponent(int top) {
+  return top < 0x100000 ? 0 : min(max((top >> 20) - 1023 + 120, 0), 254);
 }
 
 // One e4m3 code: u floor(|y| / u + d) with y = x 2^(127 - b), from the upper half of x's bits. Scaling by
 // a power of two leaves the 20 upper bits of the mantissa as they are: 3 of the code's and 17 behind
-// them. d = (2 h + 1) / 2^17 has no more bits than that, so the sum's floor is that of the truncated
-// value, an addition and a shift whose carry goes on into the exponent. Below 2^-6 the code has
-// no leading one: there the mantissa with its leading one is shifted to the fixed spacing 2^-9.
-__device__ inline unsigned e4m3(int hi, int b, unsigned h16, bool at_least_one) {
-  const int bits = hi & 0x7fffffff, e = (bits >> 20) - 1023 - (b - 127);  // exponent of y
-  const int d = (int)(2 * h16 + 1);
-  const int normal = ((bits + d) >> 17) - ((1023 + b - 127 - 7) << 3);
-  const int down = min(-6 - e, 31);
-  const int low = ((((bits & 0xfffff) | 0x100000) >> max(down, 0)) + d) >> 17;
-  int code = down > 0 ? low : normal;
-  if (at_least_one) code = max(code, 1);
-  if (bits < 0x100000) code = 0;                  // zero
-  if (bits >= 0x7ff00000) return 0x7f;            // not finite
-  return (unsigned)code | ((unsigned)hi >> 24 & 0x80u);
+// them. d = (2 h + 1) / 2^17 has no more bits than that, so the sum's floor n is that of the truncated
+// value, an addition and a shift. With e the exponent of y held to at least -6, where the mantissa is shifted to the
+// fixed spacing 2^-9, the code whose exponent field is e + 7 and whose mantissa is n - 8 is the number 8 (e + 6) + n, also
+// where n < 8 (subnormal) and where n = 16 (the next binade). Zero is shifted to nothing.
+__device__ inline unsigned e4m3(int bits, int b, unsigned d) {
+  const int e6 = (bits >> 20) - (1023 + b - 127 - 6), held = max(e6, 0), down = min(held - e6, 31);
+  const unsigned n = ((((unsigned)bits & 0xfffffu) | 0x100000u) >> down) + d;
+  return ((unsigned)held << 3) + (n >> 17);
+}
+
+// sqrt(v) rounded to nearest for v = 0 or a normal number far from the ends (squares of fp32 numbers): two steps of
+// Goldschmidt's iteration and two corrections by the residual, without the scaling that the general function needs.
+// Inf gives NaN, which a moment that is not finite becomes anyway.
+__device__ inline double root(double v) {
+  const double y = __builtin_amdgcn_rsq(v);
+  double s = v * y, h = 0.5 * y;
+  const double r = fma(-h, s, 0.5);
+  s = fma(s, r, s);
+  h = fma(h, r, h);
+  s = fma(fma(-s, s, v), h, s);
+  s = fma(fma(-s, s, v), h, s);
+  return v == 0.0 ? 0.0 : s;
 }
 
 // beta1 m + (1 - beta1) g and sqrt(beta2 r^2 + (1 - beta2) g^2), each product and the sum rounded by
@@ -87,7 +100,7 @@ __device__ inline double first_moment(double m, double g, const Hyper& h) {
 __device__ inline double second_root(double r, double g, const Hyper& h) {
 #pragma clang fp contract(off)
   const double rr = r * r, gg = g * g;
-  return sqrt(h.beta2 * rr + h.rest2 * gg);
+  return root(h.beta2 * rr + h.rest2 * gg);
 }
 
 // Four elements from e on: one wide load where all of them are there and the tensor is aligned.
@@ -172,7 +185,7 @@ struct Quad {
   }
 
   __device__ void step8(const Hyper& h, long long at) {
-    int hm[kQuad] = {}, hs[kQuad] = {}, em = -2000, es = -2000;
+    int hm[kQuad] = {}, hs[kQuad] = {}, tm = 0, ts = 0;  // upper halves of the moments, the largest magnitudes'
     if (there > 0) {
       decode4(mc, bm, m);
       decode4(sc, bs, s);
@@ -181,22 +194,37 @@ struct Quad {
         const double mj = first_moment(m[j], g[j], h), rj = second_root(s[j], g[j], h);
         p[j] = new_param(p[j], (float)mj, (float)rj, h);
         hm[j] = j < there ? __double2hiint(mj) : 0;
-        hs[j] = j < there ? __double2hiint(rj) : 0;
-        em = max(em, exponent(hm[j]));
-        es = max(es, exponent(hs[j]));
+        hs[j] = j < there ? __double2hiint(rj) & 0x7fffffff : 0;  // a NaN may have a sign
+        tm = max(tm, hm[j] & 0x7fffffff);
+        ts = max(ts, hs[j]);
       }
     }
-    em = max8(em);
-    es = max8(es);
-    bm = em == -2000 ? 0 : min(max(em + 120, 0), 254);
-    bs = es == -2000 ? 0 : min(max(es + 120, 0), 254);
+    // Seldom: what is not finite has no say in the block's exponent, counts as zero and becomes a NaN in the end.
+    const bool odd = max(tm, ts) >= kNotFinite;
+    unsigned nm = 0, ns = 0;
+    if (odd) {
+      tm = ts = 0;
+#pragma unroll
+      for (int j = 0; j < kQuad; ++j) {
+        if ((hm[j] & 0x7fffffff) >= kNotFinite) hm[j] = 0, nm |= 0x7fu << (8 * j);
+        if (hs[j] >= kNotFinite) hs[j] = 0, ns |= 0x7fu << (8 * j);
+        tm = max(tm, hm[j] & 0x7fffffff);
+        ts = max(ts, hs[j]);
+      }
+    }
+    bm = block_exponent(max8(tm));
+    bs = block_exponent(max8(ts));
     if (there <= 0) return;
-    mc = sc = 0;
+    const unsigned seed = dither_seed(at, h.key);
+    mc = nm;
+    sc = ns;
 #pragma unroll
     for (int j = 0; j < kQuad; ++j) {
-      const unsigned bits = dither_bits(at + j, h.key);
-      mc |= e4m3(hm[j], bm, bits & 0xffff, false) << (8 * j);
-      sc |= e4m3(hs[j], bs, bits >> 16, true) << (8 * j);
+      const unsigned bits = mix(seed + j * kDitherStep);
+      const unsigned cm = e4m3(hm[j] & 0x7fffffff, bm, (bits << 1 & 0x1fffeu) | 1u) | ((unsigned)hm[j] >> 24 & 0x80u);
+      const unsigned cs = max(e4m3(hs[j], bs, (bits >> 15 & 0x1fffeu) | 1u), min((unsigned)hs[j], 1u));  // 0 only for 0
+      mc |= cm << (8 * j);
+      sc |= cs << (8 * j);
     }
   }
 

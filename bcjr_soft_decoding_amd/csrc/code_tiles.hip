@@ -2,6 +2,7 @@
 // F16 and BF16: a type's variants (folds, row tiles, bits a step, tables) are a hundred kernels.
 #include <hip/hip_runtime.h>
 
+#include "code_any.h"
 #include "code_mfma.h"
 #include "ops.h"
 
@@ -86,12 +87,51 @@ int launch_tiles_any(const CodeArgs& a, int k, hipStream_t stream) {
   return launch_tiles_rows<E, 1>(a, k, stream);
 }
 
+template <class E, int F, bool IN_LDS>
+int launch_any_table(CodeArgs a, hipStream_t stream) {
+  const int steps = ((a.tile.cols + 127) / 128 + F - 1) / F;
+  const int64_t units = (a.tile.rows + 16 / F - 1) / (16 / F);
+  const size_t lds = (IN_LDS ? (size_t)4 << a.n : 0) + (size_t)kMaxWaves * kXBytes;
+  const int kw = waves_along(steps, units);
+  a.tile.kw = kw;
+  const int64_t rw = kMaxWaves / kw, blocks = (units + rw - 1) / rw;
+  const int64_t tokens = (a.tile.tokens + tile_tokens<E, F>() - 1) / tile_tokens<E, F>();
+  const void* kernel = reinterpret_cast<const void*>(k_code_any<E, F, IN_LDS>);
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return (int)e;
+  }
+  const int64_t room = 256 * (lds > kLds / 2 ? 1 : 2);
+  hipLaunchKernelGGL((k_code_any<E, F, IN_LDS>), dim3((unsigned)(blocks < room ? blocks : room), (unsigned)tokens),
+                     dim3(64 * kMaxWaves), lds, stream, a);
+  return (int)hipGetLastError();
+}
+
+template <class E, int F>
+int launch_any_fold(const CodeArgs& a, hipStream_t stream) {
+  return a.n <= 15 ? launch_any_table<E, F, true>(a, stream) : launch_any_table<E, F, false>(a, stream);
+}
+
+template <class E>
+int launch_any(const CodeArgs& a, hipStream_t stream) {
+  const int blocks = (a.tile.cols + 127) / 128;
+  if constexpr (TileOf<E>::T::kParts == 1)
+    if (a.tile.tokens == 1 && blocks > 8) return launch_any_fold<E, 16>(a, stream);
+  if constexpr (TileOf<E>::T::kParts <= 2)
+    if (a.tile.tokens <= tile_tokens<E, 8>() && blocks > 4) return launch_any_fold<E, 8>(a, stream);
+  if (a.tile.tokens <= tile_tokens<E, 4>() && blocks > 2) return launch_any_fold<E, 4>(a, stream);
+  if (a.tile.tokens <= tile_tokens<E, 2>() && blocks > 1) return launch_any_fold<E, 2>(a, stream);
+  return launch_any_fold<E, 1>(a, stream);
+}
+
 }  // namespace
 
 #define CODE_LAUNCH_(type) launch_code_tiles_##type
 #define CODE_LAUNCH(type) CODE_LAUNCH_(type)
 int CODE_LAUNCH(CODE_NAME)(const CodeArgs& a, int k, void* stream) {
-  return launch_tiles_any<CODE_TYPE>(a, k, static_cast<hipStream_t>(stream));
+  if (a.L == 0) return launch_tiles_any<CODE_TYPE>(a, k, static_cast<hipStream_t>(stream));
+  using Parts = std::conditional<std::is_same<CODE_TYPE, F16>::value, F16Parts, CODE_TYPE>::type;
+  return launch_any<Parts>(a, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace bcjr

@@ -50,19 +50,22 @@ k_code_matvec(const unsigned* __restrict__ code, long long rows, long long cols,
 
 int launch_code_matvec(int n, int k, const uint32_t* code, int64_t rows, int64_t cols, int64_t L,
                        const float* codebook, const float* scales, const MatvecIO& io, void* stream) {
-  // The matrix-core form: whole blocks of 128 columns in a chain and a table of at most 128 KiB, which leaves 8 waves
-  // the LDS they need (a codeword takes 4 bytes, 8 for fp32).
+  // On the matrix cores. Whole blocks of 128 columns in a chain and a table of at most 128 KiB, which leaves 8 waves
+  // the LDS they need (a codeword takes 4 bytes, 8 for fp32), are decoded faster than other chains of at least 8.
   const int64_t words = code_words(n, k, L);
-  if (L % 128 == 0 && n <= (io.dtype == BCJR_F32 ? 14 : 15) && k <= 4 && cols <= kTileColumns) {
+  const bool blocks = L % 128 == 0 && n <= (io.dtype == BCJR_F32 ? 14 : 15) && cols <= kTileColumns;
+  if (k <= 4 && (blocks || (L >= 8 && cols <= ((int64_t)1 << 20)))) {
     CodeArgs a;
     a.code = code;
     a.codebook = codebook;
     a.scales = scales;
     a.n = n;
+    a.k = k;
     a.chains = (int)(cols / L);
     a.words = (int)words;
-    a.per_chain = (int)(L / 128);
-    a.reciprocal = 1.0f / (float)a.per_chain;
+    a.per_chain = blocks ? (int)(L / 128) : 0;
+    a.L = blocks ? 0 : (int)L;
+    a.reciprocal = 1.0f / (float)(blocks ? a.per_chain : a.L);
     return in_pieces(io, io.dtype == BCJR_F32 ? 4 : 2, [&](const MatvecIO& piece) {
       a.tile = tile_args(piece, rows, cols);
       return io.dtype == BCJR_F32   ? launch_code_tiles_f32(a, k, stream)

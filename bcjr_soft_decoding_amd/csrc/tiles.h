@@ -38,6 +38,7 @@ struct CodeArgs {
   int n, chains, words;        // state bits; chains of a row; words of a chain
   int per_chain;               // blocks of 128 columns in a chain
   float reciprocal;            // 1 / per_chain
+  int L, k;                    // of chains in any relation to the blocks (code_any.h), with reciprocal = 1 / L
 };
 
 namespace {
@@ -63,7 +64,13 @@ struct BfTile {
 struct FloatTile : BfTile {
   static constexpr int kParts = 3;
 };
+// Halves as two bfloat16 parts, where the weights' range needs bfloat16.
+struct F16Parts : F16 {};
+struct HalfPartsTile : BfTile {
+  static constexpr int kParts = 2;
+};
 template <class E> struct TileOf;
+template <> struct TileOf<F16Parts> { using T = HalfPartsTile; };
 template <> struct TileOf<F32> { using T = FloatTile; };
 template <> struct TileOf<F16> { using T = HalfTile; };
 template <> struct TileOf<BF16> { using T = BfTile; };
@@ -208,14 +215,14 @@ struct XTile {
         if constexpr (kParts == 1) {
           *reinterpret_cast<V*>(at + x_place(r, lane & 15)) = raw[n][i];
         } else {
-          // three bfloat16 that add up to x: its leading 8 bits, the next 8 and the rest
+          // bfloat16 parts that add up to x: its leading 8 bits, the next 8 and (fp32) the rest
           u32x4 part[3];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             unsigned hi[2], mid[2], low[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float x = raw[n][i][2 * j + k];
+              const float x = (float)raw[n][i][2 * j + k];
               hi[k] = __float_as_uint(x);
               const float left = x - __uint_as_float(hi[k] & 0xffff0000u);
               mid[k] = __float_as_uint(left);
@@ -227,8 +234,8 @@ struct XTile {
           }
           if (kLoads * 4 == kTokens * F || r < kTokens * F)
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
-              *reinterpret_cast<u32x4*>(at + x_place((r / F * 3 + p) * F + r % F, lane & 15)) = part[p];
+            for (int p = 0; p < kParts; ++p)
+              *reinterpret_cast<u32x4*>(at + x_place((r / F * kParts + p) * F + r % F, lane & 15)) = part[p];
         }
       }
     in_order();

@@ -105,7 +105,7 @@ k_code_any(const CodeArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int states = 1 << a.n;
   const Pl pl;
-  char* xs = lds + (IN_LDS ? states * 4 : 0);
+  char* xs = lds + (IN_LDS ? max(states * 4, 64) : 0);
   char* mine = xs + pl.wave * kXBytes;
   const float* table = IN_LDS ? reinterpret_cast<const float*>(lds) : a.codebook;
   const int kw = a.tile.kw, ki = pl.wave % kw, ri = pl.wave / kw, rw = pl.waves / kw;

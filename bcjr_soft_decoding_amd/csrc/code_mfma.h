@@ -20,13 +20,14 @@ namespace {
 template <class E>
 struct Codeword {  // bfloat16
   static constexpr int kWords = 1;
-  static __device__ void write(unsigned* at, float c, float) {
+  static __device__ void write(unsigned* at, float c, float scale) {
+    c *= scale;
     const __bf16 hi = (__bf16)c, lo = (__bf16)(c - (float)hi);
     at[0] = (unsigned)__builtin_bit_cast(unsigned short, lo) << 16 | __builtin_bit_cast(unsigned short, hi);
   }
 };
 template <>
-struct Codeword<F16> {  // half, the codebook scaled by a power of two that brings its largest to [2^13, 2^14)
+struct Codeword<F16> {  // half
   static constexpr int kWords = 1;
   static __device__ void write(unsigned* at, float c, float scale) {
     c *= scale;
@@ -37,7 +38,8 @@ struct Codeword<F16> {  // half, the codebook scaled by a power of two that brin
 template <>
 struct Codeword<F32> {  // the leading 8 bits, the next 8, the rest
   static constexpr int kWords = 2;
-  static __device__ void write(unsigned* at, float c, float) {
+  static __device__ void write(unsigned* at, float c, float scale) {
+    c *= scale;
     const unsigned hi = __float_as_uint(c);
     const float left = c - __uint_as_float(hi & 0xffff0000u);
     const unsigned mid = __float_as_uint(left);
@@ -61,37 +63,57 @@ __device__ inline void each_codeword(const float* codebook, int states, Fn f) {
   }
 }
 
-// Exponent e of the power of two 2^-e that the half table is scaled by; codewords that are not finite
-// have no say.
-template <class E>
-__device__ inline int table_exponent(const float* codebook, int states, int* shared) {
-  if constexpr (!std::is_same<E, F16>::value) return 0;
-  if (threadIdx.x == 0) *shared = 0;
-  __syncthreads();
-  int top = 0;
-  each_codeword(codebook, states, [&](int, float c) {
-    const int e = __float_as_uint(c) >> 23 & 0xff;
-    if (e < 255) top = max(top, e);
-  });
-  for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d, 64));
-  if ((threadIdx.x & 63) == 0) atomicMax(shared, top);
-  __syncthreads();
-  const int e = *shared - 127 - 13;
-  return max(e, -126);
-}
-
 // The table in LDS, at offset 0: [2^n] codewords, or with PAIR [2^(n + K)] of two neighbours' windows.
 template <class E, int K, bool PAIR>
 struct Table {
   static constexpr int kWords = Codeword<E>::kWords * (PAIR ? 2 : 1);  // of an entry
   static constexpr int kBytes = 4 * kWords, kShift = kWords == 1 ? 2 : kWords == 2 ? 3 : 4;
   typedef unsigned Entry __attribute__((ext_vector_type(kWords)));
-  static __host__ __device__ size_t bytes(int n) { return ((size_t)kBytes << n) << (PAIR ? K : 0); }
+  static __host__ __device__ size_t bytes(int n) {
+    const size_t b = ((size_t)kBytes << n) << (PAIR ? K : 0);
+    return b < 64 ? 64 : b;
+  }
 
-  static __device__ void make(char* lds, const float* codebook, int n, float scale) {
+  // Makes the table of the codewords times 2^-e and returns e, a usual one where that brings the largest to where a
+  // half holds it well, and a chain's sum, which its scale meets only afterwards, is far from an overflow; else the e that
+  // brings it to [2^13, 2^14), in a second pass. Codewords that are not finite have no say in it. slots: LDS for a word of
+  // each wave, free again afterwards.
+  static __device__ int make(char* lds, int* slots, const float* codebook, int n) {
+    constexpr bool half = std::is_same<E, F16>::value;
+    constexpr int usual = half ? -10 : 0, least = half ? -4 : -40, most = half ? 5 : 40;  // exponents of the largest
+    int top = 0;
+    fill(lds, codebook, n, ldexpf(1.0f, -usual), [&](float c) {
+      const int bits = __float_as_uint(c) & 0x7fffffff;
+      top = max(top, bits < 0x7f800000 ? bits : 0);
+    });
+    const int e = (top >> 23) - 127;
+    // what a wave knows: whether it has seen one that is large enough, and one that is too large
+    const int seen = (__any(e >= least) ? 1 : 0) | (__any(e > most) ? 2 : 0);
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = seen;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < kMaxWaves; ++w) all |= slots[w];
+    __syncthreads();
+    if (all == 1) return usual;
+    for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d, 64));
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < kMaxWaves; ++w) top = max(top, slots[w]);
+    __syncthreads();
+    const int fit = max((top >> 23) - 127 - 13, -126);
+    fill(lds, codebook, n, ldexpf(1.0f, -fit), [](float) {});
+    __syncthreads();
+    return fit;
+  }
+
+  // see(c): every codeword, by one thread or another.
+  template <class See>
+  static __device__ void fill(char* lds, const float* codebook, int n, float scale, See see) {
+    unsigned* table = reinterpret_cast<unsigned*>(lds);
     if constexpr (!PAIR) {
       each_codeword(codebook, 1 << n, [&](int i, float c) {
-        Codeword<E>::write(reinterpret_cast<unsigned*>(lds) + i * kWords, c, scale);
+        see(c);
+        Codeword<E>::write(table + i * kWords, c, scale);
       });
     } else {
       // window i holds the states i >> K and i mod 2^n: those of one first state have neighbouring second ones
@@ -100,11 +122,12 @@ struct Table {
       for (unsigned s = threadIdx.x; s < states; s += blockDim.x) {
         const float first = codebook[s];
         const float* second = codebook + ((s << K) & (states - 1));
-        unsigned* at = reinterpret_cast<unsigned*>(lds) + (s << K) * kWords;
+        see(first);
 #pragma unroll
         for (int b = 0; b < 1 << K; ++b) {
-          Codeword<E>::write(at + b * kWords, first, scale);
-          Codeword<E>::write(at + b * kWords + Codeword<E>::kWords, second[b], scale);
+          unsigned* at = table + ((s << K) + b) * kWords;
+          Codeword<E>::write(at, first, scale);
+          Codeword<E>::write(at + Codeword<E>::kWords, second[b], scale);
         }
       }
     }
@@ -238,7 +261,6 @@ k_code_tiles(const CodeArgs a) {
   using Pl = Place<E, F>;
   constexpr int kRows = Pl::kRows, kKept = Pl::kKept;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int states = 1 << a.n;
   const Pl pl;
   using Tab = Table<E, K, PAIR>;
   char* xs = lds + Tab::bytes(a.n);  // the waves' x, behind the table
@@ -278,10 +300,7 @@ k_code_tiles(const CodeArgs a) {
     if (ki < steps) load(ki);
   };
   begin((long long)blockIdx.x * rw + ri);
-  const int top = table_exponent<E>(a.codebook, states, reinterpret_cast<int*>(xs));
-  const float down = ldexpf(1.0f, -top), up = ldexpf(1.0f, top);
-  Tab::make(lds, a.codebook, a.n, down);
-  __syncthreads();
+  const float up = ldexpf(1.0f, Tab::make(lds, reinterpret_cast<int*>(xs), a.codebook, a.n));
 
 
   for (long long ub = (long long)blockIdx.x * rw; ub < units; ub += (long long)gridDim.x * rw) {
@@ -292,14 +311,12 @@ k_code_tiles(const CodeArgs a) {
       if (s + kw < steps) load(s + kw);
       o.add(pl, lds, shift, mask, acc);
     }
-    if constexpr (std::is_same<E, F16>::value) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int u = 0; u < kKept; ++u) acc[t][n][u] *= up;
-    }
+        for (int u = 0; u < kKept; ++u) acc[t][n][u] *= up;
     if (ub + (long long)gridDim.x * rw < units) begin(ub + (long long)gridDim.x * rw + ri);
     join<E, F, RT, NT>(pl, a.tile, acc, ub, m0, xs, [](long long, const typename E::T*) { return 0.0f; });
   }

@@ -91,7 +91,7 @@ template <class E, int F, bool IN_LDS>
 int launch_any_table(CodeArgs a, hipStream_t stream) {
   const int steps = ((a.tile.cols + 127) / 128 + F - 1) / F;
   const int64_t units = (a.tile.rows + 16 / F - 1) / (16 / F);
-  const size_t lds = (IN_LDS ? (size_t)4 << a.n : 0) + (size_t)kMaxWaves * kXBytes;
+  const size_t lds = (IN_LDS ? (a.n < 4 ? 64 : (size_t)4 << a.n) : 0) + (size_t)kMaxWaves * kXBytes;
   const int kw = waves_along(steps, units);
   a.tile.kw = kw;
   const int64_t rw = kMaxWaves / kw, blocks = (units + rw - 1) / rw;

@@ -327,3 +327,92 @@ def test_products_agree_with_the_decoder():
     for t in TYPES:
         x = make_x(4, cols, t, 3)
         assert_product(bcjr.bcjr_code_matvec(x, code, cb, n, k, L), x, wh, np.abs(wh), "code", 2.0 ** -16)
+
+
+# ---- the ends of the ranges ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("L,chains", [(8, 17), (9, 15), (12, 11), (31, 9), (32, 8), (64, 5), (96, 3), (100, 21), (136, 4)])
+@pytest.mark.parametrize("t", TYPES)
+def test_code_chains_against_blocks(L, chains, t):
+    """Chains that begin anywhere within a lane's eight columns, and columns that are no multiple of eight."""
+    for n, k in ((12, 2), (7, 3), (15, 4), (16, 1)):
+        for tokens in (1, 2, 3, 5, 17):
+            log_case(f"code n={n} k={k} L={L} chains={chains} tokens={tokens} {t}")
+            code, cb, s, w = make_code(21, L * chains, n, k, L, tokens != 2, n + L)
+            x = make_x(tokens, L * chains, t, 5)
+            y = bcjr.bcjr_code_matvec(x, dev(code), dev(cb), n, k, L, None if s is None else dev(s))
+            assert_product(y, x, w, np.abs(w), "code", 2.0 ** -16 if t != "fp32" else 0.0)
+
+
+@pytest.mark.parametrize("L", [100, 128])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e4, 3e37])
+def test_code_ranges(L, size):
+    """Codewords far from 1, brought back by the scales: also beyond what a half holds."""
+    for t in TYPES:
+        log_case(f"code range {size} L={L} {t}")
+        code, cb, s, w = make_code(33, 4 * L, 9, 2, L, True, 3)
+        big = (cb.astype(np.float64) * size).astype(np.float32)
+        s2 = (s.astype(np.float64) / size).astype(np.float32)
+        w = big.astype(np.float64)[ref.code_states(code, 9, 2, L)] * s2.astype(np.float64)[:, None]
+        w = w.reshape(33, 4 * L)
+        x = make_x(4, 4 * L, t, 6)
+        y = bcjr.bcjr_code_matvec(x, dev(code), dev(big), 9, 2, L, dev(s2))
+        assert_product(y, x, w, np.abs(w), "code", 2.0 ** -16 if t != "fp32" else 0.0)
+
+
+@pytest.mark.parametrize("L", [100, 256])
+def test_non_finite_codewords_stay_in_their_rows(L):
+    log_case(f"non-finite codewords L={L}")
+    n, k, rows, cols = 10, 2, 24, 2 * L
+    code, cb, s, w = make_code(rows, cols, n, k, L, True, 4)
+    used = ref.code_states(code, n, k, L).reshape(rows, cols)
+    for bad in (np.nan, np.inf):
+        c2 = cb.copy()
+        c2[used[5, 17]] = bad
+        hit = (used == used[5, 17]).any(axis=1)
+        for t in TYPES:
+            x = make_x(3, cols, t, 8)
+            y = bcjr.bcjr_code_matvec(x, dev(code), dev(c2), n, k, L, dev(s))
+            assert not bool(torch.isfinite(y[:, hit]).any())
+            assert_product(y[:, ~hit], x, w[~hit], np.abs(w[~hit]), "code", 2.0 ** -16)
+
+
+@pytest.mark.parametrize("which", ["int4", "code"])
+def test_rows_of_x_far_apart_and_very_many_tokens(which):
+    call, w, mags, parts = product(which, 3, 96)
+    far = (1 << 24) + 40
+    for tokens in (2, 5):
+        log_case(f"{which} x stride {far} tokens={tokens}")
+        x = make_x(tokens, 96, "bf16", 2)
+        wide = torch.zeros(((tokens - 1) * far + 96,), dtype=x.dtype, device="cuda")
+        strided = wide.as_strided((tokens, 96), (far, 1))
+        strided.copy_(x)
+        assert_product(call(strided), x, w, mags, which, parts)
+    tokens = 5 * 32768 + 3
+    log_case(f"{which} tokens={tokens}")
+    few = make_x(7, 96, "fp32", 3)
+    y = call(few.repeat(tokens // 7 + 1, 1)[:tokens].contiguous())
+    for at in (0, 70000, tokens - 14):
+        at = at // 7 * 7
+        assert_product(y[at:at + 7], few, w, mags, which, parts)
+
+
+def test_longest_rows():
+    """2^24 columns in 4 bits; a chain of more columns than the tiles take."""
+    cols, group = 1 << 24, 1 << 20
+    log_case("int4 2^24 columns")
+    q = torch.zeros((2, bcjr.bcjr_int4_words(cols)), dtype=torch.int32, device="cuda")
+    codes, s, _ = make_int4(2, 512, 512, False, 3)
+    q[:, -64:] = torch.from_numpy(ref.int4_pack(codes).view(np.int32)).cuda()
+    scales = torch.zeros((2, cols // group), device="cuda")
+    scales[:, -1:] = torch.from_numpy(np.abs(s)).cuda()
+    x = torch.zeros((1, cols), device="cuda")
+    x[:, -512:] = make_x(1, 512, "fp32", 4)
+    w = ref.int4_weights(codes, np.abs(s), None, 512)
+    assert_product(bcjr.bcjr_int4_matvec(x, q.view(torch.uint32), scales, None, group), x[:, -512:], w, 32 * np.abs(s) * np.ones((2, 512)), "int4")
+    L = (1 << 20) + 64
+    log_case(f"code {L} columns")
+    code, cb, sc, w = make_code(2, L, 10, 2, L, True, 4)
+    for t in ("fp32", "bf16"):
+        x = make_x(2, L, t, 4)
+        assert_product(bcjr.bcjr_code_matvec(x, dev(code), dev(cb), 10, 2, L, dev(sc)), x, w, np.abs(w), "code", 2.0 ** -16 if t != "fp32" else 0.0)

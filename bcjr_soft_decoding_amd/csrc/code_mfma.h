@@ -48,19 +48,33 @@ struct Codeword<F32> {  // the leading 8 bits, the next 8, the rest
   }
 };
 
-// f(i, c(i)) for the block's share of the codewords, loaded four at a time, several loads in flight.
+// use(i, load(i)) for the block's share of count items, the loads of U items in flight together.
+template <int U, class Load, class Use>
+__device__ __forceinline__ void each(unsigned i, unsigned count, Load load, Use use) {
+  const unsigned block = blockDim.x;
+  for (; i + (U - 1) * block < count; i += U * block) {
+    decltype(load(i)) v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = load(i + u * block);
+#pragma unroll
+    for (int u = 0; u < U; ++u) use(i + u * block, v[u]);
+  }
+  if constexpr (U > 1) each<U / 2>(i, count, load, use);
+}
+
+// f(i, c(i)) for the block's share of the codewords, loaded four at a time.
 template <class Fn>
-__device__ inline void each_codeword(const float* codebook, int states, Fn f) {
+__device__ __forceinline__ void each_codeword(const float* codebook, int states, Fn f) {
   if (states < 4) {
     if ((int)threadIdx.x < states) f(threadIdx.x, codebook[threadIdx.x]);
     return;
   }
-#pragma unroll 4
-  for (int i = 4 * threadIdx.x; i < states; i += 4 * blockDim.x) {
-    const auto v = *reinterpret_cast<const Loose<float, 4>::V*>(codebook + i);
+  using V = typename Loose<float, 4>::V;
+  each<4>(threadIdx.x, states / 4u, [&](unsigned i) { return *reinterpret_cast<const V*>(codebook + 4 * i); },
+          [&](unsigned i, const V& v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f(i + j, v[j]);
-  }
+            for (int j = 0; j < 4; ++j) f(4 * i + j, v[j]);
+          });
 }
 
 // The table in LDS, at offset 0: [2^n] codewords, or with PAIR [2^(n + K)] of two neighbours' windows.
@@ -78,7 +92,7 @@ struct Table {
   // half holds it well, and a chain's sum, which its scale meets only afterwards, is far from an overflow; else the e that
   // brings it to [2^13, 2^14), in a second pass. Codewords that are not finite have no say in it. slots: LDS for a word of
   // each wave, free again afterwards.
-  static __device__ int make(char* lds, int* slots, const float* codebook, int n) {
+  static __device__ __forceinline__ int make(char* lds, int* slots, const float* codebook, int n) {
     constexpr bool half = std::is_same<E, F16>::value;
     constexpr int usual = half ? -10 : 0, least = half ? -4 : -40, most = half ? 5 : 40;  // exponents of the largest
     int top = 0;
@@ -108,7 +122,7 @@ struct Table {
 
   // see(c): every codeword, by one thread or another.
   template <class See>
-  static __device__ void fill(char* lds, const float* codebook, int n, float scale, See see) {
+  static __device__ __forceinline__ void fill(char* lds, const float* codebook, int n, float scale, See see) {
     unsigned* table = reinterpret_cast<unsigned*>(lds);
     if constexpr (!PAIR) {
       each_codeword(codebook, 1 << n, [&](int i, float c) {
@@ -117,19 +131,28 @@ struct Table {
       });
     } else {
       // window i holds the states i >> K and i mod 2^n: those of one first state have neighbouring second ones
+      struct Windows {
+        float first, second[1 << K];
+      };
       const unsigned states = 1u << n;
-#pragma unroll 4
-      for (unsigned s = threadIdx.x; s < states; s += blockDim.x) {
-        const float first = codebook[s];
-        const float* second = codebook + ((s << K) & (states - 1));
-        see(first);
+      each<(K <= 2 ? 4 : 1)>(
+          threadIdx.x, states,
+          [&](unsigned s) {
+            Windows v;
+            v.first = codebook[s];
 #pragma unroll
-        for (int b = 0; b < 1 << K; ++b) {
-          unsigned* at = table + ((s << K) + b) * kWords;
-          Codeword<E>::write(at, first, scale);
-          Codeword<E>::write(at + Codeword<E>::kWords, second[b], scale);
-        }
-      }
+            for (int b = 0; b < 1 << K; ++b) v.second[b] = codebook[((s << K) & (states - 1)) + b];
+            return v;
+          },
+          [&](unsigned s, const Windows& v) {
+            see(v.first);
+#pragma unroll
+            for (int b = 0; b < 1 << K; ++b) {
+              unsigned* at = table + ((s << K) + b) * kWords;
+              Codeword<E>::write(at, v.first, scale);
+              Codeword<E>::write(at + Codeword<E>::kWords, v.second[b], scale);
+            }
+          });
     }
   }
 };

@@ -3,6 +3,8 @@
 // window of its chain, and from the start of the next chain where that begins among the eight (L >= 8). Chains and so
 // scales may change anywhere in a sum, so the scale is multiplied into the weight, in fp32, before it is taken apart
 // into bfloat16 parts. Halves are multiplied as two bfloat16 parts: scale times codeword may leave their range.
+// Bound by unpacking and by the table's reads: 8192 x 8200 in chains of 100 with 16 tokens takes 82 us; with S = 2^16,
+// whose table stays in memory, 8192 x 8192 takes 271 us.
 #pragma once
 #include "code_mfma.h"
 

@@ -68,7 +68,7 @@ __device__ inline void load_w8(const typename E::T* row, long long c, long long 
 
 // LG lanes for a group, a lane for 8 columns: loaded once where the group has no more (ONCE), else
 // once for the range and once for the codes. Bound by memory: 2048 x 8192 fp32 weights are read and
-// their codes written at 4.0 TB/s.
+// their codes written in 21 us, at 3.5 TB/s; a small matrix by its loads' and reductions' latency (1000 x 4100 bf16 9 us).
 template <class E, bool ONCE, bool ZEROS>
 __global__ void __launch_bounds__(256)
 k_int4_quantize(const typename E::T* __restrict__ w, long long rows, int cols, int group, int groups, int words, int lg,

@@ -12,7 +12,8 @@
 namespace bcjr {
 namespace {
 
-// Any shape: one wave for a row and TB tokens, a lane for a column.
+// Any shape: one wave for a row and TB tokens, a lane for a column. For what the tiles do not take; bound by its 64-bit
+// addresses and one table read a weight (2048 x 8192 with k = 8 and one token 103 us).
 template <class E, int TB>
 __global__ void __launch_bounds__(256)
 k_code_matvec(const unsigned* __restrict__ code, long long rows, long long cols, long long L, int n,

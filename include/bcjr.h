@@ -342,8 +342,8 @@ bcjr_status bcjr_dense_backward(int32_t S, const float* theta, const float* code
  * once to the type of y. Tokens and output rows are independent, and a token's outputs do not
  * depend on how many others the call holds within the types' precision (not bitwise: the tile that
  * is used goes by the number of tokens). A NaN or Inf in x makes that token's outputs NaN or Inf
- * (Inf may become NaN); one in a scale or in a codeword does so for the rows it scales or for every
- * output. These calls need no workspace and may be captured into a graph.
+ * (Inf may become NaN); one in a scale or in a codeword does so for the rows that use it. These
+ * calls need no workspace and may be captured into a graph.
  */
 typedef enum { BCJR_F32 = 0, BCJR_F16 = 1, BCJR_BF16 = 2 } bcjr_dtype; /* IEEE half; bfloat16 */
 
@@ -402,7 +402,8 @@ bcjr_status bcjr_int4_dequantize(const uint32_t* q, const float* scales, const u
 /*
  * Products with 4-bit weights; x, y, strides, types and errors as in bcjr_code_matvec.
  * q DEVICE, 16-byte aligned (BCJR_E_ARG otherwise); zeros DEVICE or NULL (z = 8; z > 15 is not
- * checked and stands for itself).
+ * checked and stands for itself). A group's sum of |x|, for which the zero point is taken off at the end, may
+ * not pass 2^126: an output may be NaN then.
  */
 bcjr_status bcjr_int4_matvec(const uint32_t* q, const float* scales, const uint8_t* zeros,
                              int64_t rows, int64_t cols, int64_t group, const void* x,

@@ -8,6 +8,8 @@ together stay below lambda sqrt(n + 8) 2^-24 A but with a probability of 2 exp(-
 zero point may be summed as before they are subtracted (each at most 16 units). A codeword may be held
 as two 16-bit parts for 16-bit x: 2^-16 of each term on top, worst case.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -416,3 +418,43 @@ def test_longest_rows():
     for t in ("fp32", "bf16"):
         x = make_x(2, L, t, 4)
         assert_product(bcjr.bcjr_code_matvec(x, dev(code), dev(cb), 10, 2, L, dev(sc)), x, w, np.abs(w), "code", 2.0 ** -16 if t != "fp32" else 0.0)
+
+
+@pytest.mark.parametrize("n,k,L,cols", [(12, 2, 256, 4096), (15, 2, 256, 4096), (15, 1, 100, 4100), (16, 2, 64, 4096)])
+def test_captured_large_tables(n, k, L, cols):
+    """Tables beyond 64 KiB of LDS, and in memory: eager, from two host threads at once, on their streams, and
+    captured give the same bits."""
+    rows = 2056
+    code, cb, s, w = make_code(rows, cols, n, k, L, True, 8)
+    cd, cbd, sd = dev(code), dev(cb), dev(s)
+    call = lambda x, y=None: bcjr.bcjr_code_matvec(x, cd, cbd, n, k, L, sd, y=y)  # noqa: E731
+    for t, tokens in (("bf16", 1), ("fp16", 5), ("fp32", 2)):
+        log_case(f"large table n={n} k={k} L={L} {t} tokens={tokens}")
+        xs = [make_x(tokens, cols, t, 30 + i) for i in range(3)]
+        eager = [call(x) for x in xs]
+        torch.cuda.synchronize()
+        assert_product(eager[0], xs[0], w, np.abs(w), "code", 2.0 ** -16 if t != "fp32" else 0.0)
+        results = [None, None]
+
+        def work(i):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                results[i] = [call(x) for x in xs]
+                torch.cuda.current_stream().synchronize()
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for th in threads:
+            th.start()
+        for th in threads:
+            th.join()
+        xin, yout = xs[0].clone(), torch.empty_like(eager[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(xin, y=yout)
+        for i, x in enumerate(xs):
+            assert all(torch.equal(r[i], eager[i]) for r in results)
+            xin.copy_(x)
+            graph.replay()
+            again = call(x)
+            torch.cuda.synchronize()
+            assert torch.equal(yout, eager[i]) and torch.equal(again, eager[i])

@@ -151,6 +151,10 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+# The current device's number; callers hold tensors on a device, so torch has been initialised.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 class _NoSwitch:
     """The context of a call whose device is the current one already."""
 
@@ -166,7 +170,7 @@ _NO_SWITCH = _NoSwitch()
 
 def _on(device):
     """The context that a call on this device is made in."""
-    return _NO_SWITCH if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NO_SWITCH if device.index == _current_device() else torch.cuda.device(device)
 
 
 def trellis(n: int, k: int, codebook=None, v: int = 1) -> Trellis:
@@ -681,12 +685,12 @@ def bcjr_int4_quantize(w, group, with_zeros=False):
         raise ValueError("w has no columns")
     dev = _device(w)
     groups = -(-cols // group)
-    q = torch.empty((rows, bcjr_int4_words(cols)), dtype=U32, device=dev)
-    scales = torch.empty((rows, groups), dtype=F32, device=dev)
-    zeros = torch.empty((rows, groups), dtype=U8, device=dev) if with_zeros else None
+    q = w.new_empty((rows, (cols + 127) // 128 * 16), dtype=U32)
+    scales = w.new_empty((rows, groups), dtype=F32)
+    zeros = w.new_empty((rows, groups), dtype=U8) if with_zeros else None
     with _on(dev):
-        st = lib().bcjr_int4_quantize(_ptr(w), dt, rows, cols, group, _ptr(q), _ptr(scales),
-                                      _ptr(zeros), _stream(dev))
+        st = lib().bcjr_int4_quantize(w.data_ptr(), dt, rows, cols, group, q.data_ptr(), scales.data_ptr(),
+                                      None if zeros is None else zeros.data_ptr(), _stream(dev))
     _check(st, "bcjr_int4_quantize")
     return q, scales, zeros
 

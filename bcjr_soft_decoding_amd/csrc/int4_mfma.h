@@ -6,8 +6,8 @@
 // 16 scale (D - (1 + z / 16) S), in fp32: nothing is rounded before the last conversion.
 //
 // One token is bound by memory where the matrix is large (16384 x 16384 in 34.5 us, 4.1 TB/s) and by latency where it is
-// not (2048 x 8192 5.5 us, 512 x 1024 3.2). 32 tokens through 16384 x 16384 take 55 us: 28 of memory, 16 of unpacking and 9
-// of products, which the 2 waves a SIMD that the registers leave room for overlap in part.
+// not (2048 x 8192 5.5 us, 512 x 1024 3.2). 32 tokens through 16384 x 16384 take 55 us: 28 of memory, 18 of LDS, 16 of
+// unpacking and 9 of products, which the 2 waves a SIMD that the registers leave room for overlap in part.
 #pragma once
 #include "tiles.h"
 

@@ -285,3 +285,20 @@ def test_autograd_sees_the_update():
                          step=1, lr=1e-3)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+@pytest.mark.parametrize("gt", ["bf16", "fp32"])
+def test_moments_right_at_borders(gt):
+    """Gradients that are small whole multiples of the block's unit: a moment is then often a power of two,
+    or on a code's border, up to its last bit, and codes and exponents are the formula's all the same."""
+    log_case(f"adamw borders {gt}")
+    n = 1 << 18
+    c = Case([n], "fp32", gt, 8, 9)
+    rng = np.random.default_rng(10)
+    unit = np.ldexp(1.0, c.ms.cpu().numpy().astype(int).repeat(32) - 127)
+    g = torch.from_numpy(unit * rng.integers(-128, 129, n)).cuda()
+    c.g[0].copy_(g)
+    assert torch.equal(c.g[0].double(), g)
+    c.vs.copy_(c.ms)
+    for step in (3, 4):
+        c.check(hyper(step=step, seed=step))
